@@ -27,13 +27,16 @@ QMM_ERR_DTYPE, QMM_ERR_DEVICE, QMM_ERR_CUDA, QMM_ERR_DEVICE_CHECK = 5, 6, 7, 8
 STATUS_NAMES = {0: "QMM_OK", 1: "QMM_ERR_NULL", 2: "QMM_ERR_SHAPE", 3: "QMM_ERR_BLOCK", 4: "QMM_ERR_ALIGN",
                 5: "QMM_ERR_DTYPE", 6: "QMM_ERR_DEVICE", 7: "QMM_ERR_CUDA", 8: "QMM_ERR_DEVICE_CHECK"}
 QMM_Q8_0, QMM_Q4_0 = 0, 1
+QMM_F32, QMM_BF16 = 0, 1
 QMM_FLAG_EARLY_WEIGHTS = 1
 BLOCK = 32
 MAX_DECODE_M = 8
 MAX_K = 32768
 MAX_PROJ = 4
+KV_MAX_QUERIES = 8
 
 _i64, _int, _u32, _p = ctypes.c_int64, ctypes.c_int, ctypes.c_uint32, ctypes.c_void_p
+_f32 = ctypes.c_float
 _SIGS = {
     "qmm_q8_gemv": [_i64, _i64, _i64, _int, _p, _p, _p, _p],
     "qmm_q8_gemv_ex": [_i64, _i64, _i64, _int, _p, _p, _p, _u32, _p],
@@ -56,6 +59,12 @@ _SIGS = {
     "qmm_q8q8_gemv_fused_dots": [_i64, _i64, _i64, _int, _p, _p, _p, _p, _p, _p, _p],
     "qmm_q8q8_block_dots_q8_0": [_i64, _i64, _i64, _int, _p, _p, _p, _p],
     "qmm_test_withheld_copy": [_int, _i64, _i64, _i64, _int, _p, _p, _p, ctypes.c_uint64, _p],
+    "qmm_kv_page_bytes": [_int, _int, _i64, _i64, _int, _i64, _p],
+    "qmm_kv_write": [_int, _int, _int, _i64, _i64, _i64, _int, _i64, _i64, _p, _i64, _i64, _p, _i64, _i64, _p, _p, _p],
+    "qmm_kv_read": [_int, _int, _int, _i64, _i64, _i64, _int, _i64, _i64, _p, _p, _p, _p, _p],
+    "qmm_kv_attn": [_int, _int, _int, _i64, _i64, _i64, _i64, _i64, _int, _i64, _i64, _p, _i64, _i64, _i64, _p, _p,
+                    _i64, _i64, _p, _f32, _i64, _p, _p, _i64, _p],
+    "qmm_kv_attn_workspace": [_i64, _i64, _i64, _i64, _i64, _p],
 }
 for _name, _args in _SIGS.items():
     _f = getattr(lib, _name, None)
@@ -306,3 +315,156 @@ def qmm_prefill_plan(wtype: int, M: int, N: int, K: int, *, block: int = BLOCK) 
     _check(lib.qmm_prefill_plan(wtype, M, N, K, block, ctypes.addressof(out)), "qmm_prefill_plan")
     return {"mt": out[0], "split": out[1], "stages": out[2], "ctas": out[3],
             "kernel": "small_m" if out[4] == 1 else "tcgen05"}
+
+
+# ---- quantised key/value cache ---------------------------------------------
+
+_KV_DTYPES = {torch.float32: QMM_F32, torch.bfloat16: QMM_BF16}
+
+
+def _need(ok: bool, fn: str, what: str):
+    if not ok:
+        raise ValueError(f"{fn}: {what}")
+
+
+def _kv_cache(fn: str, cache: torch.Tensor, Hkv: int, D: int, page: int, ktype: int, vtype: int, block: int) -> int:
+    """Pages of a cache tensor (uint8 [pages, page_bytes], contiguous), checked against its form."""
+    _need(cache.dtype == torch.uint8 and cache.dim() == 2 and cache.is_contiguous(), fn,
+          "cache is not a contiguous uint8 tensor [pages, page_bytes]")
+    size = qmm_kv_page_bytes(Hkv, D, page=page, ktype=ktype, vtype=vtype, block=block)
+    _need(cache.shape[1] == size, fn, f"pages of {cache.shape[1]} bytes, this form has {size}")
+    return cache.shape[0]
+
+
+def _kv_rows(fn: str, name: str, t: torch.Tensor, dims: int, like: torch.Tensor):
+    _need(t.dim() == dims and (t.stride(-1) == 1 or t.shape[-1] == 1 or t.numel() == 0), fn,
+          f"{name} is not a tensor of {dims} dims with contiguous rows")
+    _need(t.dtype in _KV_DTYPES, fn, f"{name} is {t.dtype}, not float32 or bfloat16")
+    _need(t.device == like.device, fn, f"{name} is on {t.device}, the cache on {like.device}")
+
+
+def _strides(t: torch.Tensor, dims: int):
+    """Strides of the leading dims; 0 where a dim is not stepped over (its stride is arbitrary)."""
+    return [t.stride(i) if t.shape[i] > 1 and t.numel() else 0 for i in range(dims)]
+
+
+def _kv_index(fn: str, name: str, t: torch.Tensor, dtype, like: torch.Tensor):
+    _need(t.dtype == dtype and t.device == like.device, fn, f"{name} is not a {dtype} tensor on {like.device}")
+
+
+class _KvCall:
+    """Device and stream of a call: the tensors' device is made the current one, and what the call
+    allocates belongs to the stream that it runs on."""
+
+    def __init__(self, like: torch.Tensor, stream):
+        self.dev = like.device
+        if self.dev.type != "cuda":
+            self.ctx, self.stream = None, 0 if stream is None else _stream(stream)
+            return
+        here = self.dev.index == torch.cuda.current_device()
+        if stream is None:
+            self.ctx = None if here else torch.cuda.device(self.dev)
+            self.stream = torch.cuda.current_stream(self.dev).cuda_stream
+        else:
+            if isinstance(stream, int):
+                stream = torch.cuda.ExternalStream(stream, device=self.dev) if stream else torch.cuda.default_stream(self.dev)
+            _need(stream.device == self.dev, "stream", f"the stream is on {stream.device}, the tensors on {self.dev}")
+            self.ctx, self.stream = torch.cuda.stream(stream), stream.cuda_stream
+
+    def __enter__(self):
+        if self.ctx is not None:
+            self.ctx.__enter__()
+        return self.stream
+
+    def __exit__(self, *exc):
+        if self.ctx is not None:
+            self.ctx.__exit__(*exc)
+
+
+def qmm_kv_page_bytes(Hkv: int, D: int, *, page: int, ktype: int = QMM_Q4_0, vtype: int = QMM_Q4_0,
+                      block: int = BLOCK) -> int:
+    """Bytes of a page of a key/value cache of this form."""
+    out = ctypes.c_int64(0)
+    _check(lib.qmm_kv_page_bytes(ktype, vtype, Hkv, D, block, page, ctypes.addressof(out)), "qmm_kv_page_bytes")
+    return out.value
+
+
+def qmm_kv_write(cache: torch.Tensor, K: torch.Tensor, V: torch.Tensor, slots: torch.Tensor, *, page: int,
+                 ktype: int = QMM_Q4_0, vtype: int = QMM_Q4_0, block: int = BLOCK, stream=None) -> torch.Tensor:
+    """Quantise K, V [T, Hkv, D] (fp32 or bf16, rows contiguous) into the cache's slots int64 [T] (negative: left
+    out; the others have to differ). cache: uint8 [pages, qmm_kv_page_bytes(Hkv, D, ...)]."""
+    fn = "qmm_kv_write"
+    _kv_rows(fn, "K", K, 3, cache)
+    _kv_rows(fn, "V", V, 3, cache)
+    T, Hkv, D = K.shape
+    _need(V.shape == K.shape and V.dtype == K.dtype, fn, "V is not of K's shape and type")
+    _kv_index(fn, "slots", slots, torch.int64, cache)
+    _need(slots.shape == (T,) and slots.is_contiguous(), fn, f"slots is not a contiguous tensor of {T}")
+    pages = _kv_cache(fn, cache, Hkv, D, page, ktype, vtype, block)
+    with _KvCall(cache, stream) as s:
+        _check(lib.qmm_kv_write(ktype, vtype, _KV_DTYPES[K.dtype], T, Hkv, D, block, pages, page, K.data_ptr(),
+                                *_strides(K, 2), V.data_ptr(), *_strides(V, 2), slots.data_ptr(), cache.data_ptr(),
+                                s), fn)
+    return cache
+
+
+def qmm_kv_read(cache: torch.Tensor, slots: torch.Tensor, Hkv: int, D: int, K: torch.Tensor | None = None,
+                V: torch.Tensor | None = None, *, page: int, ktype: int = QMM_Q4_0, vtype: int = QMM_Q4_0,
+                dtype: torch.dtype = torch.float32, block: int = BLOCK, stream=None):
+    """(K, V) [T, Hkv, D]: the values of the cached tokens at slots int64 [T] (rows of a negative slot are left as
+    they were). dtype: float32 or bfloat16, that of K and V where they are given."""
+    fn = "qmm_kv_read"
+    T = slots.shape[0]
+    _kv_index(fn, "slots", slots, torch.int64, cache)
+    _need(slots.dim() == 1 and slots.is_contiguous(), fn, "slots is not a contiguous tensor of one dim")
+    pages = _kv_cache(fn, cache, Hkv, D, page, ktype, vtype, block)
+    with _KvCall(cache, stream) as s:
+        K = _out(K, (T, Hkv, D), cache.device, dtype)
+        V = _out(V, (T, Hkv, D), cache.device, dtype)
+        for name, t in (("K", K), ("V", V)):
+            _kv_rows(fn, name, t, 3, cache)
+            _need(t.shape == (T, Hkv, D) and t.is_contiguous(), fn, f"{name} is not a contiguous {(T, Hkv, D)}")
+        _need(K.dtype == V.dtype, fn, "K and V differ in type")
+        _check(lib.qmm_kv_read(ktype, vtype, _KV_DTYPES[K.dtype], T, Hkv, D, block, pages, page, slots.data_ptr(),
+                               cache.data_ptr(), K.data_ptr(), V.data_ptr(), s), fn)
+    return K, V
+
+
+def qmm_kv_attn_workspace(B: int, M: int, Hq: int, Hkv: int, D: int) -> int:
+    """Scratch bytes of qmm_kv_attn for these sizes."""
+    out = ctypes.c_int64(0)
+    _check(lib.qmm_kv_attn_workspace(B, M, Hq, Hkv, D, ctypes.addressof(out)), "qmm_kv_attn_workspace")
+    return out.value
+
+
+def qmm_kv_attn(Q: torch.Tensor, cache: torch.Tensor, table: torch.Tensor, lens: torch.Tensor, Hkv: int,
+                Y: torch.Tensor | None = None, ws: torch.Tensor | None = None, *, page: int, ktype: int = QMM_Q4_0,
+                vtype: int = QMM_Q4_0, scale: float | None = None, window: int = 0, block: int = BLOCK,
+                stream=None) -> torch.Tensor:
+    """Y [B, M, Hq, D]: attention of the M <= 8 query tokens Q [B, M, Hq, D] (fp32 or bf16, rows contiguous) of each
+    sequence, its last M tokens, over its lens int32 [B] cached tokens; table int32 [B, max_pages] names the pages.
+    scale: D ** -0.5 by default; window: how many keys a query sees (0: all up to its own). ws: uint8 scratch of
+    qmm_kv_attn_workspace(...) bytes, allocated by default; calls that may run at the same time need their own."""
+    fn = "qmm_kv_attn"
+    _kv_rows(fn, "Q", Q, 4, cache)
+    B, M, Hq, D = Q.shape
+    _kv_index(fn, "table", table, torch.int32, cache)
+    _need(table.dim() == 2 and table.shape[0] == B and (table.shape[1] <= 1 or table.stride(1) == 1), fn,
+          f"table is not a tensor of {B} contiguous rows")
+    _kv_index(fn, "lens", lens, torch.int32, cache)
+    _need(lens.shape == (B,) and lens.is_contiguous(), fn, f"lens is not a contiguous tensor of {B}")
+    pages = _kv_cache(fn, cache, Hkv, D, page, ktype, vtype, block)
+    need = qmm_kv_attn_workspace(B, M, Hq, Hkv, D)
+    with _KvCall(cache, stream) as s:
+        Y = _out(Y, (B, M, Hq, D), cache.device, Q.dtype)
+        _need(Y.shape == Q.shape and Y.dtype == Q.dtype and Y.device == cache.device and Y.is_contiguous(), fn,
+              "Y is not a contiguous tensor of Q's shape, type and device")
+        if ws is None:
+            ws = torch.empty(need, dtype=torch.uint8, device=cache.device)
+        _need(ws.dtype == torch.uint8 and ws.is_contiguous() and ws.device == cache.device, fn,
+              "ws is not a contiguous uint8 tensor on the cache's device")
+        _check(lib.qmm_kv_attn(ktype, vtype, _KV_DTYPES[Q.dtype], B, M, Hq, Hkv, D, block, pages, page, Q.data_ptr(),
+                               *_strides(Q, 3), cache.data_ptr(), table.data_ptr(), *_strides(table, 1),
+                               table.shape[1], lens.data_ptr(), D ** -0.5 if scale is None else scale,
+                               window, Y.data_ptr(), ws.data_ptr(), ws.numel(), s), fn)
+    return Y

@@ -1,0 +1,90 @@
+// kv_layout.cuh -- where each byte of the quantised key/value cache lies
+// (include/qmm.h, "Quantised key/value cache"), shared by the kernels that
+// write it, read it back and attend to it.
+//
+// The cache is pages of `page` tokens; a page holds, for each key/value head,
+// page / 16 groups of 16 tokens, and a group its key codes, key scales, value
+// codes and value scales, one contiguous run of bytes whose length is a
+// multiple of 16: one bulk copy brings a group, or several that follow each
+// other in a page. Inside a group the codes stand in the order in which the
+// lanes of a warp feed them to mma.m16n8k16 (lane = 4 g + t, g < 8, t < 4):
+//
+//  * keys are the columns of the first product. Column n of the group's half j
+//    is token (n >> 1) + 4 (n & 1) + 8 j, and lane (g, t) of column g needs
+//    dims 4t .. 4t+3 and 16+4t .. 16+4t+3 of every block, so these bytes stand
+//    together for as many blocks as fill 16 bytes (4 of Q4_0, 2 of Q8_0) and
+//    the chunks of the 32 lanes follow each other: 128-bit loads without a
+//    bank conflict;
+//  * values are the columns of the second product, so lane (g, t) needs dims
+//    2g, 2g+1, 16+2g and 17+2g of every block of tokens t, t+4, t+8, t+12:
+//    8-byte chunks for 4 (2) blocks, and the chunks that 16 lanes load
+//    together follow each other;
+//  * a scale of each of the four tokens t, t+4, t+8, t+12 is 8 bytes together,
+//    for every block of t.
+//
+// A head size whose block count is not a multiple of 4 (2) is laid out in runs
+// of 4 (2), then 2, then 1 blocks.
+#pragma once
+
+#include <stdint.h>
+
+namespace qmm {
+
+constexpr int kKvGroup = 16;  // tokens of a group
+
+// Bytes of the keys' (or the values') part of a group: codes, then scales.
+__host__ __device__ constexpr int kv_code_bytes(int nb, bool q8) { return nb * (q8 ? 512 : 256); }
+__host__ __device__ constexpr int kv_part_bytes(int nb, bool q8) { return kv_code_bytes(nb, q8) + nb * 32; }
+
+struct KvRun {
+  int first, n;  // first block of the run, its blocks
+};
+
+// The run of blocks that block b belongs to.
+__host__ __device__ constexpr KvRun kv_run(int nb, bool q8, int b) {
+  int first = 0, n = q8 ? 2 : 4;
+  while (b >= first + n || first + n > nb) {
+    if (first + n <= nb)
+      first += n;
+    else
+      n >>= 1;
+  }
+  return KvRun{first, n};
+}
+
+// Byte offset in the part of code byte x (ggml order: 32 of a Q8_0 block, 16 of
+// a Q4_0 block) of block b of token tok (0..15).
+__host__ __device__ constexpr int kv_key_code_at(int nb, bool q8, int tok, int b, int x) {
+  const KvRun r = kv_run(nb, q8, b);
+  const int row = 8 * (tok >> 3) + 2 * (tok & 3) + ((tok >> 2) & 1);
+  if (q8) return r.first * 512 + ((row * 4 + (x & 15) / 4) * r.n + b - r.first) * 8 + (x >> 4) * 4 + (x & 3);
+  return r.first * 256 + ((row * 4 + x / 4) * r.n + b - r.first) * 4 + (x & 3);
+}
+
+__host__ __device__ constexpr int kv_val_code_at(int nb, bool q8, int tok, int b, int x) {
+  const KvRun r = kv_run(nb, q8, b);
+  const int g = (x & 15) >> 1, unit = q8 ? 4 : 2;
+  const int chunk = r.n * unit == 8 ? ((g >> 2) * 64 + tok * 4 + (g & 3)) * 8 : (tok * 8 + g) * r.n * unit;
+  return r.first * (q8 ? 512 : 256) + chunk + (b - r.first) * unit + (x >> 4) * 2 + (x & 1);
+}
+
+// Byte offset in the part of the fp16 scale of block b of token tok.
+__host__ __device__ constexpr int kv_scale_at(int nb, bool q8, int tok, int b) {
+  return kv_code_bytes(nb, q8) + ((tok & 3) * nb + b) * 8 + (tok >> 2) * 2;
+}
+
+// A cache's form, as the kernels use it.
+struct KvForm {
+  int nb;            // blocks of a row: head size / 32
+  int heads;         // key/value heads
+  int page;          // tokens of a page (a power of two, 16 at least)
+  bool kq8, vq8;     // Q8_0 (else Q4_0)
+  int64_t pages;
+  __host__ __device__ int group_bytes() const { return kv_part_bytes(nb, kq8) + kv_part_bytes(nb, vq8); }
+  // Offset of group `grp` (of page * heads * groups order) in the cache.
+  __host__ __device__ int64_t group_at(int64_t pg, int head, int grp) const {
+    return ((pg * heads + head) * (page / kKvGroup) + grp) * static_cast<int64_t>(group_bytes());
+  }
+};
+
+}  // namespace qmm

@@ -1,12 +1,14 @@
 // qmm_api.cu -- the extern "C" entry points of libqmm.so: argument validation
 // (host only, before any CUDA call), device checks and dispatch to the
 // kernel launchers. The operations themselves are defined in include/qmm.h.
+#include <math.h>
 #include <stdarg.h>
 #include <stdio.h>
 
 #include <mutex>
 #include <string>
 
+#include "kv_layout.cuh"
 #include "qmm_internal.h"
 
 namespace qmm {
@@ -397,6 +399,155 @@ static qmm_status prefill_impl(int wtype, int64_t M, int64_t N, int64_t K, int b
   return launch_prefill(dev, wtype, M, N, static_cast<int>(K), W, X, Y, s, flags);
 }
 
+// ---- quantised key/value cache ---------------------------------------------
+
+// Checks of a cache's form; fills *f.
+static qmm_status check_kv_form(const char *fn, int ktype, int vtype, int64_t Hkv, int64_t D, int block, int64_t pages,
+                                int64_t page, KvForm *f) {
+  if (block != QMM_BLOCK) return set_error(QMM_ERR_BLOCK, "%s: block=%d, only 32 is supported", fn, block);
+  for (int t : {ktype, vtype})
+    if (t != QMM_Q8_0 && t != QMM_Q4_0) return set_error(QMM_ERR_DTYPE, "%s: unknown cache type %d", fn, t);
+  if (Hkv < 1 || Hkv > QMM_KV_MAX_HEADS)
+    return set_error(QMM_ERR_SHAPE, "%s: Hkv=%lld outside 1..%d", fn, (long long)Hkv, QMM_KV_MAX_HEADS);
+  if (D != 64 && D != 96 && D != 128 && D != 192 && D != 256)
+    return set_error(QMM_ERR_SHAPE, "%s: D=%lld is not 64, 96, 128, 192 or 256", fn, (long long)D);
+  if (page < 16 || page > 65536 || (page & (page - 1)))
+    return set_error(QMM_ERR_SHAPE, "%s: page=%lld is not a power of two from 16 to 65536", fn, (long long)page);
+  if (pages < 0 || pages > INT32_MAX)
+    return set_error(QMM_ERR_SHAPE, "%s: pages=%lld outside 0..2^31-1", fn, (long long)pages);
+  f->nb = static_cast<int>(D / 32);
+  f->heads = static_cast<int>(Hkv);
+  f->page = static_cast<int>(page);
+  f->kq8 = ktype == QMM_Q8_0;
+  f->vq8 = vtype == QMM_Q8_0;
+  f->pages = pages;
+  return QMM_OK;
+}
+
+static qmm_status check_dtype(const char *fn, int dtype) {
+  if (dtype != QMM_F32 && dtype != QMM_BF16) return set_error(QMM_ERR_DTYPE, "%s: unknown element type %d", fn, dtype);
+  return QMM_OK;
+}
+
+// Strides in elements: rows have to stay on 16-byte boundaries.
+static qmm_status check_stride(const char *fn, const char *name, int64_t stride, int dtype) {
+  if (stride < 0 || stride > (int64_t(1) << 40))
+    return set_error(QMM_ERR_SHAPE, "%s: stride %s=%lld outside 0..2^40", fn, name, (long long)stride);
+  if (stride * (dtype == QMM_F32 ? 4 : 2) % 16)
+    return set_error(QMM_ERR_ALIGN, "%s: stride %s=%lld elements is not a multiple of 16 bytes", fn, name,
+                     (long long)stride);
+  return QMM_OK;
+}
+
+static qmm_status kv_write_impl(int ktype, int vtype, int dtype, int64_t T, int64_t Hkv, int64_t D, int block,
+                                int64_t pages, int64_t page, const void *K, int64_t k_tok, int64_t k_head,
+                                const void *V, int64_t v_tok, int64_t v_head, const int64_t *slots, void *cache,
+                                qmm_stream_t stream) {
+  const char *fn = "qmm_kv_write";
+  t_last_error.clear();
+  KvForm f;
+  QMM_TRY(check_kv_form(fn, ktype, vtype, Hkv, D, block, pages, page, &f));
+  QMM_TRY(check_dtype(fn, dtype));
+  if (T < 0 || T > INT32_MAX) return set_error(QMM_ERR_SHAPE, "%s: T=%lld outside 0..2^31-1", fn, (long long)T);
+  QMM_TRY(check_stride(fn, "k_tok", k_tok, dtype));
+  QMM_TRY(check_stride(fn, "k_head", k_head, dtype));
+  QMM_TRY(check_stride(fn, "v_tok", v_tok, dtype));
+  QMM_TRY(check_stride(fn, "v_head", v_head, dtype));
+  if (T == 0) return QMM_OK;
+  QMM_TRY(check_ptr(fn, "K", K, true, 16));
+  QMM_TRY(check_ptr(fn, "V", V, true, 16));
+  QMM_TRY(check_ptr(fn, "slots", slots, true, 8));
+  QMM_TRY(check_ptr(fn, "cache", cache, pages > 0, 16));
+  DevInfo dev;
+  QMM_TRY(current_device(&dev));
+  return launch_kv_write(dev, f, dtype, T, K, k_tok, k_head, V, v_tok, v_head, slots, cache,
+                         reinterpret_cast<cudaStream_t>(stream));
+}
+
+static qmm_status kv_read_impl(int ktype, int vtype, int dtype, int64_t T, int64_t Hkv, int64_t D, int block,
+                               int64_t pages, int64_t page, const int64_t *slots, const void *cache, void *K, void *V,
+                               qmm_stream_t stream) {
+  const char *fn = "qmm_kv_read";
+  t_last_error.clear();
+  KvForm f;
+  QMM_TRY(check_kv_form(fn, ktype, vtype, Hkv, D, block, pages, page, &f));
+  QMM_TRY(check_dtype(fn, dtype));
+  if (T < 0 || T > INT32_MAX) return set_error(QMM_ERR_SHAPE, "%s: T=%lld outside 0..2^31-1", fn, (long long)T);
+  if (T == 0) return QMM_OK;
+  QMM_TRY(check_ptr(fn, "slots", slots, true, 8));
+  QMM_TRY(check_ptr(fn, "cache", cache, pages > 0, 16));
+  QMM_TRY(check_ptr(fn, "K", K, true, 16));
+  QMM_TRY(check_ptr(fn, "V", V, true, 16));
+  DevInfo dev;
+  QMM_TRY(current_device(&dev));
+  return launch_kv_read(dev, f, dtype, T, slots, cache, K, V, reinterpret_cast<cudaStream_t>(stream));
+}
+
+static qmm_status check_kv_queries(const char *fn, int64_t B, int64_t M, int64_t Hq, int64_t Hkv) {
+  if (B < 0 || B > QMM_KV_MAX_BATCH)
+    return set_error(QMM_ERR_SHAPE, "%s: B=%lld outside 0..%d", fn, (long long)B, QMM_KV_MAX_BATCH);
+  if (M < 0 || M > QMM_KV_MAX_QUERIES)
+    return set_error(QMM_ERR_SHAPE, "%s: M=%lld outside 0..%d", fn, (long long)M, QMM_KV_MAX_QUERIES);
+  if (Hq < 1 || Hq % Hkv != 0 || Hq / Hkv > QMM_KV_MAX_RATIO)
+    return set_error(QMM_ERR_SHAPE, "%s: Hq=%lld is not 1..%d times Hkv=%lld", fn, (long long)Hq, QMM_KV_MAX_RATIO,
+                     (long long)Hkv);
+  return QMM_OK;
+}
+
+static qmm_status kv_attn_impl(int ktype, int vtype, int dtype, int64_t B, int64_t M, int64_t Hq, int64_t Hkv,
+                               int64_t D, int block, int64_t pages, int64_t page, const void *Q, int64_t q_seq,
+                               int64_t q_tok, int64_t q_head, const void *cache, const int32_t *table,
+                               int64_t table_stride, int64_t max_pages, const int32_t *lens, float scale,
+                               int64_t window, void *Y, void *ws, int64_t ws_bytes, qmm_stream_t stream) {
+  const char *fn = "qmm_kv_attn";
+  t_last_error.clear();
+  KvForm f;
+  QMM_TRY(check_kv_form(fn, ktype, vtype, Hkv, D, block, pages, page, &f));
+  QMM_TRY(check_dtype(fn, dtype));
+  QMM_TRY(check_kv_queries(fn, B, M, Hq, Hkv));
+  QMM_TRY(check_stride(fn, "q_seq", q_seq, dtype));
+  QMM_TRY(check_stride(fn, "q_tok", q_tok, dtype));
+  QMM_TRY(check_stride(fn, "q_head", q_head, dtype));
+  if (max_pages < 0 || max_pages >= (int64_t(1) << 30) / page)
+    return set_error(QMM_ERR_SHAPE, "%s: max_pages=%lld with page=%lld reaches 2^30 tokens", fn, (long long)max_pages,
+                     (long long)page);
+  if (table_stride < 0 || table_stride > (int64_t(1) << 40))
+    return set_error(QMM_ERR_SHAPE, "%s: table_stride=%lld outside 0..2^40", fn, (long long)table_stride);
+  if (window < 0) return set_error(QMM_ERR_SHAPE, "%s: window=%lld is negative", fn, (long long)window);
+  if (!isfinite(scale)) return set_error(QMM_ERR_SHAPE, "%s: scale is not finite", fn);
+  if (B == 0 || M == 0) return QMM_OK;
+  QMM_TRY(check_ptr(fn, "Q", Q, true, 16));
+  QMM_TRY(check_ptr(fn, "cache", cache, pages > 0, 16));
+  QMM_TRY(check_ptr(fn, "table", table, max_pages > 0, 4));
+  QMM_TRY(check_ptr(fn, "lens", lens, true, 4));
+  QMM_TRY(check_ptr(fn, "Y", Y, true, 16));
+  QMM_TRY(check_ptr(fn, "ws", ws, true, 16));
+  const int64_t need = 4 * kv_attn_workspace_floats(B, static_cast<int>(M), static_cast<int>(Hq),
+                                                    static_cast<int>(Hkv), static_cast<int>(D));
+  if (ws_bytes < need)
+    return set_error(QMM_ERR_SHAPE, "%s: ws_bytes=%lld, %lld are needed", fn, (long long)ws_bytes, (long long)need);
+  DevInfo dev;
+  QMM_TRY(current_device(&dev));
+  KvAttnArgs a{};
+  a.q = Q;
+  a.cache = static_cast<const uint8_t *>(cache);
+  a.table = table;
+  a.lens = lens;
+  a.out = Y;
+  a.ws = static_cast<float *>(ws);
+  a.q_seq = q_seq;
+  a.q_tok = q_tok;
+  a.q_head = q_head;
+  a.table_stride = table_stride;
+  a.batch = static_cast<int>(B);
+  a.m = static_cast<int>(M);
+  a.hq = static_cast<int>(Hq);
+  a.max_pages = static_cast<int>(max_pages);
+  a.window = window >= (int64_t(1) << 30) ? 0 : static_cast<int>(window);  // longer than any sequence: none
+  a.scale = scale;
+  return launch_kv_attn(dev, f, dtype, a, reinterpret_cast<cudaStream_t>(stream));
+}
+
 }  // namespace qmm
 
 using namespace qmm;
@@ -526,6 +677,52 @@ QMM_API qmm_status qmm_prefill_plan(int wtype, int64_t M, int64_t N, int64_t K, 
   return QMM_OK;
 }
 
+QMM_API qmm_status qmm_kv_page_bytes(int ktype, int vtype, int64_t Hkv, int64_t D, int block, int64_t page,
+                                     int64_t *bytes) {
+  const char *fn = "qmm_kv_page_bytes";
+  t_last_error.clear();
+  if (bytes == nullptr) return set_error(QMM_ERR_NULL, "%s: bytes is NULL", fn);
+  KvForm f;
+  QMM_TRY(check_kv_form(fn, ktype, vtype, Hkv, D, block, 0, page, &f));
+  *bytes = static_cast<int64_t>(f.heads) * (f.page / kKvGroup) * f.group_bytes();
+  return QMM_OK;
+}
+
+QMM_API qmm_status qmm_kv_write(int ktype, int vtype, int dtype, int64_t T, int64_t Hkv, int64_t D, int block,
+                                int64_t pages, int64_t page, const void *K, int64_t k_tok, int64_t k_head,
+                                const void *V, int64_t v_tok, int64_t v_head, const int64_t *slots, void *cache,
+                                qmm_stream_t stream) {
+  return kv_write_impl(ktype, vtype, dtype, T, Hkv, D, block, pages, page, K, k_tok, k_head, V, v_tok, v_head, slots,
+                       cache, stream);
+}
+
+QMM_API qmm_status qmm_kv_read(int ktype, int vtype, int dtype, int64_t T, int64_t Hkv, int64_t D, int block,
+                               int64_t pages, int64_t page, const int64_t *slots, const void *cache, void *K, void *V,
+                               qmm_stream_t stream) {
+  return kv_read_impl(ktype, vtype, dtype, T, Hkv, D, block, pages, page, slots, cache, K, V, stream);
+}
+
+QMM_API qmm_status qmm_kv_attn(int ktype, int vtype, int dtype, int64_t B, int64_t M, int64_t Hq, int64_t Hkv,
+                               int64_t D, int block, int64_t pages, int64_t page, const void *Q, int64_t q_seq,
+                               int64_t q_tok, int64_t q_head, const void *cache, const int32_t *table,
+                               int64_t table_stride, int64_t max_pages, const int32_t *lens, float scale,
+                               int64_t window, void *Y, void *ws, int64_t ws_bytes, qmm_stream_t stream) {
+  return kv_attn_impl(ktype, vtype, dtype, B, M, Hq, Hkv, D, block, pages, page, Q, q_seq, q_tok, q_head, cache, table,
+                      table_stride, max_pages, lens, scale, window, Y, ws, ws_bytes, stream);
+}
+
+QMM_API qmm_status qmm_kv_attn_workspace(int64_t B, int64_t M, int64_t Hq, int64_t Hkv, int64_t D, int64_t *bytes) {
+  const char *fn = "qmm_kv_attn_workspace";
+  t_last_error.clear();
+  if (bytes == nullptr) return set_error(QMM_ERR_NULL, "%s: bytes is NULL", fn);
+  KvForm f;
+  QMM_TRY(check_kv_form(fn, QMM_Q4_0, QMM_Q4_0, Hkv, D, QMM_BLOCK, 0, 16, &f));
+  QMM_TRY(check_kv_queries(fn, B, M, Hq, Hkv));
+  *bytes = 4 * kv_attn_workspace_floats(B, static_cast<int>(M), static_cast<int>(Hq), static_cast<int>(Hkv),
+                                        static_cast<int>(D));
+  return QMM_OK;
+}
+
 QMM_API const char *qmm_last_error_string(void) { return t_last_error.c_str(); }
 
 QMM_API const char *qmm_version(void) { return "qmm 0.1.0 sm_100a"; }
@@ -543,6 +740,12 @@ QMM_API qmm_status qmm_device_status(uint32_t *bits) {
   if (e != cudaSuccess) return cuda_check(e, "status read");
   *bits |= b;
   e = prefill_status(&b);
+  if (e != cudaSuccess) return cuda_check(e, "status read");
+  *bits |= b;
+  e = kv_cache_status(&b);
+  if (e != cudaSuccess) return cuda_check(e, "status read");
+  *bits |= b;
+  e = kv_attn_status(&b);
   if (e != cudaSuccess) return cuda_check(e, "status read");
   *bits |= b;
   if (*bits) return set_error(QMM_ERR_DEVICE_CHECK, "qmm_device_status: a kernel recorded a failure (bits 0x%x)", *bits);

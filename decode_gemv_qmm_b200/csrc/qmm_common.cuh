@@ -10,11 +10,13 @@
 
 namespace qmm {
 
-// Bits OR-ed into a kernel file's device status word when a bounded wait gives up.
+// Bits OR-ed into a kernel file's device status word when a bounded wait gives
+// up or an index in device memory is out of range.
 enum : uint32_t {
   kDevTimeoutFull = 1u,   // a stage never became full (its copy never landed)
   kDevTimeoutDrain = 2u,  // a copy still in flight could not be drained on the error path
   kDevTimeoutMma = 4u,    // a tensor-core commit never arrived
+  kDevBadIndex = 8u,      // a slot, page number or length read from device memory was out of range
 };
 
 // Give up on a barrier after this many nanoseconds (kernels here run for

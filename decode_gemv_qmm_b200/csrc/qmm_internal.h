@@ -105,9 +105,32 @@ qmm_status launch_prefill(const DevInfo &dev, int wtype, int64_t M, int64_t N, i
 qmm_status launch_prefill_small_withheld(const DevInfo &dev, int wtype, int64_t M, int64_t N, int K, const void *W,
                                          const uint16_t *X, float *Y, uint64_t wait_ns, cudaStream_t stream);
 
+// ---- quantised key/value cache (kv_layout.cuh) ----------------------------
+struct KvForm;
+struct KvAttnArgs {
+  const void *q;
+  const uint8_t *cache;
+  const int32_t *table, *lens;
+  void *out;
+  float *ws;
+  int64_t q_seq, q_tok, q_head, table_stride;
+  int batch, m, hq, max_pages, window;
+  float scale;
+};
+qmm_status launch_kv_write(const DevInfo &dev, const KvForm &f, int dtype, int64_t T, const void *K, int64_t kst,
+                           int64_t ksh, const void *V, int64_t vst, int64_t vsh, const int64_t *slots, void *cache,
+                           cudaStream_t stream);
+qmm_status launch_kv_read(const DevInfo &dev, const KvForm &f, int dtype, int64_t T, const int64_t *slots,
+                          const void *cache, void *K, void *V, cudaStream_t stream);
+qmm_status launch_kv_attn(const DevInfo &dev, const KvForm &f, int dtype, const KvAttnArgs &a, cudaStream_t stream);
+// Scratch floats of launch_kv_attn.
+int64_t kv_attn_workspace_floats(int64_t batch, int m, int hq, int hkv, int d);
+
 // Device status word of each kernel file: read and clear (synchronous).
 cudaError_t q8_gemv_status(uint32_t *bits);
 cudaError_t q4_gateup_status(uint32_t *bits);
 cudaError_t prefill_status(uint32_t *bits);
+cudaError_t kv_cache_status(uint32_t *bits);
+cudaError_t kv_attn_status(uint32_t *bits);
 
 }  // namespace qmm

@@ -82,13 +82,16 @@ typedef enum {
   QMM_ERR_SHAPE = 2,        /* negative size, K % 32 != 0, M or K too large  */
   QMM_ERR_BLOCK = 3,        /* block != 32                                    */
   QMM_ERR_ALIGN = 4,        /* pointer not aligned as documented              */
-  QMM_ERR_DTYPE = 5,        /* unknown weight type                            */
+  QMM_ERR_DTYPE = 5,        /* unknown weight or element type                 */
   QMM_ERR_DEVICE = 6,       /* current device is not compute capability 10.x  */
   QMM_ERR_CUDA = 7,         /* a CUDA runtime call failed                      */
   QMM_ERR_DEVICE_CHECK = 8  /* a kernel recorded a device-side failure         */
 } qmm_status;
 
 typedef enum { QMM_Q8_0 = 0, QMM_Q4_0 = 1 } qmm_wtype;
+
+/* Element types of the key/value cache's entry points. */
+typedef enum { QMM_F32 = 0, QMM_BF16 = 1 } qmm_dtype;
 
 #define QMM_BLOCK 32
 #define QMM_Q8_0_BLOCK_BYTES 34
@@ -100,6 +103,13 @@ typedef enum { QMM_Q8_0 = 0, QMM_Q4_0 = 1 } qmm_wtype;
 #define QMM_MAX_K 32768
 /* Most projections per qmm_q8_gemv_multi call. */
 #define QMM_MAX_PROJ 4
+
+/* Limits of the key/value cache's entry points: sequences of a call, query
+ * tokens of a sequence, query heads of a key/value head, key/value heads. */
+#define QMM_KV_MAX_BATCH 65536
+#define QMM_KV_MAX_QUERIES 8
+#define QMM_KV_MAX_RATIO 128
+#define QMM_KV_MAX_HEADS 1024
 
 /* Option of the *_ex entry points: start streaming the weight blocks before
  * the preceding kernel in the stream has finished (programmatic dependent
@@ -358,6 +368,130 @@ QMM_API qmm_status qmm_quant_matmul_prefill_ex(int wtype, int64_t M, int64_t N, 
                                                const void *W, const uint16_t *X, float *Y, uint32_t flags,
                                                qmm_stream_t stream);
 
+/*
+ * ---------------------------------------------------------------------------
+ * Quantised key/value cache
+ *
+ * Keys and values of a decoder's tokens, held in the block formats of the
+ * weights (Q8_0 or Q4_0, keys and values each of their own type), written as
+ * tokens arrive and read where they lie by the attention. Element types: fp32
+ * (the decode path's) or bf16 (the prefill path's); sums, maxima and products
+ * are fp32 either way.
+ *
+ * Form of a cache, common to the calls below:
+ *   ktype, vtype  QMM_Q8_0 or QMM_Q4_0 (QMM_ERR_DTYPE otherwise)
+ *   Hkv           key/value heads, 1 .. QMM_KV_MAX_HEADS
+ *   D             head size: 64, 96, 128, 192 or 256
+ *   page          tokens of a page, a power of two from 16 to 65536
+ *   pages         pages of the cache; a slot is page_index * page + place
+ *   cache         pages * qmm_kv_page_bytes(...) bytes (device, 16-byte aligned)
+ *
+ * Layout. A page holds, head by head, page / 16 groups of 16 tokens; a group
+ * holds key codes, key scales, value codes and value scales (16 D + D bytes for
+ * Q8_0, 8 D + D for Q4_0, each). Token place p is token tok = p % 16 of group
+ * p / 16. With blk = tok's block b of 32 dims, in ggml's order of code bytes x
+ * (Q8_0: byte x is dim x; Q4_0: byte x is dims x and, in the high nibble, x +
+ * 16), a group's blocks are laid out in runs of n = 4 (Q4_0) or 2 (Q8_0) blocks,
+ * a remainder in runs of 2, then 1; `first` is a run's first block:
+ *   key code   Q8_0  512 first + ((4 row + (x % 16) / 4) n + b - first) 8 + (x / 16) 4 + x % 4
+ *              Q4_0  256 first + ((4 row + x / 4) n + b - first) 4 + x % 4
+ *              row = 8 (tok / 8) + 2 (tok % 4) + (tok / 4) % 2
+ *   value code with u = 4 (Q8_0) or 2 (Q4_0) and g = (x % 16) / 2:
+ *              128 u first + c + (b - first) u + (x / 16) 2 + x % 2, where
+ *              c = (64 (g / 4) + 4 tok + g % 4) 8 if n u == 8, else (8 tok + g) n u
+ *   scale      (fp16) behind the codes: ((tok % 4) D / 32 + b) 8 + (tok / 4) 2
+ * (the order in which the attention's tensor-core tiles take them).
+ *
+ * Slots and page numbers are device data, so the host cannot check them: a
+ * slot or page that does not exist is left out by the kernels, which record it
+ * (bit 8 of qmm_device_status()).
+ * ---------------------------------------------------------------------------
+ */
+
+/* qmm_kv_page_bytes -- bytes of one page of a cache of this form (host only,
+ * needs no device). *bytes: host, written. */
+QMM_API qmm_status qmm_kv_page_bytes(int ktype, int vtype, int64_t Hkv, int64_t D, int block, int64_t page,
+                                     int64_t *bytes);
+
+/*
+ * qmm_kv_write -- quantise the keys and values of T tokens into the cache.
+ *
+ * Each 32-block of a row by ggml's rules, every step an IEEE binary32
+ * operation: Q8_0 as qmm_quantize_act_q8_0; Q4_0 with m the first x_j of
+ * largest magnitude, d = m / -8, id = 1 / d (0 when d == 0), q_j = min(15,
+ * trunc(x_j * id + 8.5)). The scale is stored as binary16(d), rounded to
+ * nearest even. The stored bytes are a function of the row alone.
+ *
+ *   dtype     QMM_F32 or QMM_BF16: elements of K and V
+ *   T         tokens, >= 0
+ *   K, V      row (token i, head h) at K + i * k_tok + h * k_head, in elements
+ *             (device, read only); D elements each, contiguous. Pointers and
+ *             strides are multiples of 16 bytes.
+ *   slots     T int64 (device): where each token goes; a negative slot leaves
+ *             the token out. Slots >= 0 of one call have to differ: what a slot
+ *             named twice holds afterwards is unspecified (each byte is one of
+ *             the tokens')
+ *   cache     written at the slots' tokens; every other byte is left as it was
+ */
+QMM_API qmm_status qmm_kv_write(int ktype, int vtype, int dtype, int64_t T, int64_t Hkv, int64_t D, int block,
+                                int64_t pages, int64_t page, const void *K, int64_t k_tok, int64_t k_head,
+                                const void *V, int64_t v_tok, int64_t v_head, const int64_t *slots, void *cache,
+                                qmm_stream_t stream);
+
+/*
+ * qmm_kv_read -- the values that T cached tokens stand for: code * scale,
+ * exact in fp32, rounded once (to nearest even) to bf16.
+ *
+ *   dtype     QMM_F32 or QMM_BF16: elements of K and V
+ *   slots     T int64 (device), in any order, repeated or not; the rows of a
+ *             negative slot are left as they were
+ *   K, V      T x Hkv x D (device, 16-byte aligned, written)
+ */
+QMM_API qmm_status qmm_kv_read(int ktype, int vtype, int dtype, int64_t T, int64_t Hkv, int64_t D, int block,
+                               int64_t pages, int64_t page, const int64_t *slots, const void *cache, void *K, void *V,
+                               qmm_stream_t stream);
+
+/*
+ * qmm_kv_attn -- decode attention: M query tokens of each of B sequences over
+ * the sequences' pages of the cache.
+ *
+ * Query token i (0 .. M-1) of sequence s is the token at position
+ * lens[s] - M + i; with k_j, v_j the cached values of position j,
+ *   Y[s][i][h] = sum_j p_j v_j / sum_j p_j,  p_j = exp(scale * (Q[s][i][h] . k_j) - max_j),
+ *   over 0 <= j <= lens[s] - M + i and, if window > 0, j > lens[s] - M + i - window,
+ * where query head h belongs to key/value head h / (Hq / Hkv). A row that sees
+ * no key is 0. Cached tokens past lens[s] are never used, whatever they hold.
+ *
+ *   dtype     QMM_F32 or QMM_BF16: elements of Q and Y
+ *   B, M      sequences (<= QMM_KV_MAX_BATCH) and query tokens of each
+ *             (<= QMM_KV_MAX_QUERIES); 0 = empty call
+ *   Hq        query heads, Hq / Hkv whole and <= QMM_KV_MAX_RATIO
+ *   Q         row (s, i, h) at Q + s * q_seq + i * q_tok + h * q_head, in
+ *             elements (device, read only); pointer and strides multiples of 16 bytes
+ *   table     page numbers (device, int32): page t of sequence s at
+ *             table[s * table_stride + t], t < max_pages; entries past a
+ *             sequence's tokens are not read. max_pages * page < 2^30
+ *   lens      B int32 (device): cached tokens of each sequence, the M query
+ *             tokens' own among them; 0 .. max_pages * page
+ *   scale     factor of the scores, finite (e.g. 1 / sqrt(D))
+ *   window    >= 0; 0 = none
+ *   Y         B x M x Hq x D (device, 16-byte aligned, written)
+ *   ws        ws_bytes >= qmm_kv_attn_workspace(...) bytes of scratch (device,
+ *             16-byte aligned, no contents needed before or after); one call at
+ *             a time may use it
+ * A position whose page does not exist is left out, a length outside the range
+ * is taken as the nearest one in it; both are recorded (qmm_device_status).
+ */
+QMM_API qmm_status qmm_kv_attn(int ktype, int vtype, int dtype, int64_t B, int64_t M, int64_t Hq, int64_t Hkv,
+                               int64_t D, int block, int64_t pages, int64_t page, const void *Q, int64_t q_seq,
+                               int64_t q_tok, int64_t q_head, const void *cache, const int32_t *table,
+                               int64_t table_stride, int64_t max_pages, const int32_t *lens, float scale,
+                               int64_t window, void *Y, void *ws, int64_t ws_bytes, qmm_stream_t stream);
+
+/* qmm_kv_attn_workspace -- scratch bytes that qmm_kv_attn needs for these sizes
+ * (host only, needs no device). *bytes: host, written. */
+QMM_API qmm_status qmm_kv_attn_workspace(int64_t B, int64_t M, int64_t Hq, int64_t Hkv, int64_t D, int64_t *bytes);
+
 /* ------------------------------------------------------------------------ */
 /* Test and utility exports (not on the hot path).                           */
 
@@ -451,7 +585,8 @@ QMM_API const char *qmm_version(void);
  * the device-side status words that kernels set when a bounded wait gives up.
  * *bits receives their OR (0 = no failure recorded; 1 = a copy or stage never
  * arrived, 2 = a copy in flight could not be drained on the error path, 4 = a
- * tensor-core commit never arrived). Returns QMM_OK when *bits == 0,
+ * tensor-core commit never arrived, 8 = a slot, page number or length of a
+ * key/value cache call was out of range). Returns QMM_OK when *bits == 0,
  * QMM_ERR_DEVICE_CHECK when a failure was recorded, or QMM_ERR_CUDA if the
  * synchronisation itself failed.
  */
