@@ -1,0 +1,10 @@
+// kv_attn_d64.cu -- instances of the decode attention kernel for head size 64.
+#include "kv_attn.cuh"
+
+namespace qmm {
+
+cudaError_t kv_attn_d64(const DevInfo &dev, KvLaunch &p, uint32_t *status, const cudaLaunchConfig_t &cfg) {
+  return kv_attn_types<2>(dev, p, status, cfg);
+}
+
+}  // namespace qmm

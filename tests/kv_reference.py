@@ -121,10 +121,11 @@ class Cache:
 
 
 def attention(q, k, v, length, scale, window=0):
-    """One sequence. q [M, Hq, d], k, v [length, Hkv, d], all float64 -> (out, A, S): the result, sum p|v| / sum p
-    per output, and per row the largest sum |scale q_d k_jd| over its keys."""
+    """One sequence. q [M, Hq, d], k, v [length, Hkv, d], all float64 -> (out, A, S, F): the result, sum p|v| / sum p
+    per output, per row the largest sum |scale q_d k_jd| over its keys, and the keys times the largest |v|."""
     m, hq, d = q.shape
     out, a, s = np.zeros(q.shape), np.zeros(q.shape), np.zeros((m, hq, 1))
+    floor = len(v) * np.abs(v).max(initial=0.0)
     ratio = hq // (k.shape[1] if k.ndim == 3 else 1)
     for i in range(m):
         last = length - m + i
@@ -138,7 +139,7 @@ def attention(q, k, v, length, scale, window=0):
             p /= p.sum()
             out[i, h], a[i, h] = p @ vv, p @ np.abs(vv)
             s[i, h] = (np.abs(kk) @ np.abs(q[i, h])).max() * abs(scale)
-    return out, a, s
+    return out, a, s, floor
 
 
 def assert_attention(got, ref, what="", bf16=False):
@@ -153,13 +154,22 @@ def assert_attention(got, ref, what="", bf16=False):
     16 u sqrt(1 + D) A to that in the same sense. bf16 outputs are rounded once
     more: 2^-8 of the value. Over a whole output the errors do not line up: its
     2-norm is held to 1e-5 of A's, the library's fp32 tolerance.
+
+    The weights p d_v are held as two fp16 terms, at a power of two that brings
+    the largest scale d_v of the keys to 2^14 or more. fp16's smallest step is
+    2^-24, so a weight is off by 2^-25 at least there, that is 2^-39 of the
+    largest d_v, and its product with a code c by 2^-39 |c| max d_v <= 2^-39 *
+    128/127 max|v| (the largest |c| is 8 or 127 and belongs to the largest |v| of
+    its block). Each of the keys may add one such error to an output, and sum p
+    >= 1 divides them: F 2^-38 with F = keys * max|v| covers it. It counts where
+    everything that a dim sees weighs less than about 2^-39.
     """
-    out, a, s = ref
+    out, a, s, floor = ref
     got = np.asarray(got, dtype=np.float64)
     assert got.shape == out.shape, (what, got.shape, out.shape)
     assert np.isfinite(got).all(), f"{what}: non-finite outputs"
     u, d = 2.0 ** -24, got.shape[-1]
-    bound = (16 * u * np.sqrt(d) * s + 16 * u * np.sqrt(1 + d)) * a + (2.0 ** -8 * np.abs(out) if bf16 else 0)
+    bound = (16 * u * np.sqrt(d) * s + 16 * u * np.sqrt(1 + d)) * a + 2.0 ** -38 * floor + (2.0 ** -8 * np.abs(out) if bf16 else 0)
     err = np.abs(got - out)
     bad = err > bound
     if bad.any():
