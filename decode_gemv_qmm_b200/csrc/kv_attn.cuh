@@ -22,33 +22,31 @@ __device__ __forceinline__ float exp2_approx(float x) {
   return y;
 }
 
-// C += A . B, 16 x 8 x 16, fp16 operands, fp32 sums.
-__device__ __forceinline__ void mma_f16(float (&c)[4], const uint4 &a, uint32_t b0, uint32_t b1) {
-  asm volatile(
-      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
-      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-      : "r"(a.x), "r"(a.y), "r"(a.z), "r"(a.w), "r"(b0), "r"(b1));
+// D = A . B + C, 16 x 8 x 16, fp16 operands, fp32 sums.
+__device__ __forceinline__ float4 mma_f16(const uint4 &a, uint32_t b0, uint32_t b1, const float4 &c) {
+  float4 d;
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%11,%12,%13};"
+      : "=f"(d.x), "=f"(d.y), "=f"(d.z), "=f"(d.w)
+      : "r"(a.x), "r"(a.y), "r"(a.z), "r"(a.w), "r"(b0), "r"(b1), "f"(c.x), "f"(c.y), "f"(c.z), "f"(c.w));
+  return d;
 }
 
 // Two fp32 values as fp16 pairs hi + lo: 22 bits of each, when they are neither
 // above 65504 nor so small that lo falls below fp16's 2^-24.
-__device__ __forceinline__ void split_f16(float x, float y, uint32_t &hi, uint32_t &lo) {
-  const __half2 h = __floats2half2_rn(x, y);
-  const float2 f = __half22float2(h);
-  hi = h2_bits(h);
-  lo = h2_bits(__floats2half2_rn(x - f.x, y - f.y));
+__device__ __forceinline__ void split_f16(float2 x, __half2 &hi, __half2 &lo) {
+  hi = __float22half2_rn(x);
+  lo = __float22half2_rn(__ffma2_rn(__half22float2(hi), make_float2(-1.0f, -1.0f), x));
 }
 
 // Codes as fp16 pairs, exact: 0x6400 | c is 1024 + c.
-//  low nibbles of bytes 0 and 2 of w
+//   Q4_0: low nibbles of bytes 0 and 2 of w; high nibbles of bytes 0 and 2
 __device__ __forceinline__ uint32_t q4_low(uint32_t w) {
   return h2_bits(__hsub2(bits_h2((w & 0x000f000fu) | 0x64006400u), bits_h2(0x64086408u)));  // - 1032
 }
-//  high nibbles of bytes 0 and 2 of w: (1024 + 16 c) / 16 - 72
 __device__ __forceinline__ uint32_t q4_high(uint32_t w) {
-  return h2_bits(__hfma2(bits_h2((w & 0x00f000f0u) | 0x64006400u), bits_h2(0x2c002c00u), bits_h2(0xd480d480u)));
+  return h2_bits(__hfma2(bits_h2((w & 0x00f000f0u) | 0x64006400u), bits_h2(0x2c002c00u), bits_h2(0xd480d480u)));  // / 16 - 72
 }
-//  two bytes of w (already xor 0x80808080) chosen by sel, as codes
+//   Q8_0: two bytes of w (already xor 0x80808080: code + 128) chosen by kSel
 template <uint32_t kSel>
 __device__ __forceinline__ uint32_t q8_pair(uint32_t w) {
   return h2_bits(__hsub2(bits_h2(__byte_perm(w, 0x64646464u, kSel)), bits_h2(0x64806480u)));  // - 1152
@@ -65,31 +63,51 @@ __device__ __forceinline__ uint2 lds_u2(uint32_t addr) {
 // Floats of one partial result: rows x (D + maximum and sum).
 __host__ __device__ constexpr int64_t kv_attn_slot_floats(int rows, int d) { return static_cast<int64_t>(rows) * (d + 2); }
 
-// What the main kernel tells the joining kernel about block c's last item.
+// An item that begins in a block and ends in a later one: what the second launch joins.
 struct KvSplit {
-  int seq, head, tile, last;  // seq < 0: nothing to join; last: the block that holds the item's end
+  int seq, head, tile, last;  // seq < 0: none; last: the block that holds the item's end
 };
 
-constexpr int kKvMaxBlocks = 1184;   // most blocks of a launch
-constexpr int kKvRowsMax = 32;       // most rows of a partial result
+constexpr int kKvMaxBlocks = 160;  // most blocks of a launch
+constexpr int kKvMaxWarps = 8;     // most warps of a block
+#ifndef KV_ITEM_COST
+#define KV_ITEM_COST 4
+#endif
+constexpr int kKvItemCost = KV_ITEM_COST;  // what beginning an item costs, in groups
 
-template <int NB, bool KQ8, bool VQ8, int MT>
+// Scratch: the blocks' KvSplit, two partial results of each block, two of each warp.
+__host__ __device__ constexpr int64_t kv_attn_scratch_floats(int rows, int d) {
+  return kKvMaxBlocks * (4 + 2 * (1 + kKvMaxWarps) * kv_attn_slot_floats(rows, d));
+}
+
+template <int NB, bool KQ8, bool VQ8, int OCT, bool FINE>
 struct KvCfg {
   static constexpr int kD = NB * 32;
   static constexpr int kKeyPart = kv_part_bytes(NB, KQ8);
   static constexpr int kGroupBytes = kKeyPart + kv_part_bytes(NB, VQ8);
-  static constexpr int kTG = kGroupBytes <= 4608 ? 2 : 1;  // groups of a step
+  static constexpr int kRows = 8 * OCT;
+  static constexpr int kMT = FINE ? OCT : (OCT + 1) / 2;  // 16-row tiles: eight rows in two terms, or sixteen
+  static constexpr int kQBytes = kMT * NB * 1024;         // a warp's query fragments
+  static constexpr int kBudget = 222 * 1024;
+#ifndef KV_TG
+#define KV_TG 2
+#endif
+#ifndef KV_NW
+#define KV_NW 8
+#endif
+  static constexpr int warp_bytes(int tg, int stages) { return kQBytes + stages * tg * kGroupBytes; }
+  static constexpr int kNW = KV_NW * warp_bytes(1, 2) <= kBudget ? KV_NW : KV_NW / 2;
+  static constexpr int kTG = kGroupBytes <= 4608 && kNW * warp_bytes(KV_TG, 2) <= kBudget ? KV_TG : 1;  // groups of a step
+  static constexpr int stages() {
+    int n = 2;
+    while (n < 4 && kNW * warp_bytes(kTG, n + 1) <= kBudget) ++n;
+    return n;
+  }
+  static constexpr int kStages = stages();
   static constexpr int kStageBytes = kTG * kGroupBytes;
-  static constexpr int kRowPad = kD + 16;                  // floats of a row in the joining buffer
-  static constexpr int kRows = 8 * MT;
-  static constexpr int kQBytes = MT * NB * 1024;
-  static constexpr int kFixed = kQBytes + 1024;            // query fragments, barriers, statistics
-  static constexpr int warp_bytes(int stages) { return stages * kStageBytes + 8 * kRowPad * 4; }
-  static constexpr int kBudget = 220 * 1024 - kFixed;
-  static constexpr int kNW = 8 * warp_bytes(2) <= kBudget ? 8 : 4;
-  static constexpr int kStages = kNW * warp_bytes(4) <= kBudget ? 4 : kNW * warp_bytes(3) <= kBudget ? 3 : 2;
-  static constexpr int kSmem = kFixed + kNW * warp_bytes(kStages);
-  static_assert(kNW * warp_bytes(kStages) <= kBudget, "stages do not fit");
+  static constexpr int kSmem = kNW * warp_bytes(kTG, kStages);
+  static_assert(kSmem <= kBudget, "stages do not fit");
+  static_assert(kNW <= kKvMaxWarps, "scratch is sized for fewer warps");
 };
 
 // A launch's constants.
@@ -97,7 +115,7 @@ struct KvLaunch {
   KvForm f;
   KvAttnArgs a;
   int ratio, rows, tiles;  // query heads of a key/value head; rows M ratio of one; tiles of kRows rows
-  int min_groups;          // least groups of a block
+  int min_units;           // least units of the line for a warp
   int bf16;
 };
 
@@ -121,6 +139,9 @@ __device__ __forceinline__ KvSeq kv_seq(const KvLaunch &p, int s, uint32_t *stat
   return q;
 }
 
+// Units of the line that an item of n groups takes.
+__device__ __forceinline__ int64_t kv_units(int n) { return n ? n + kKvItemCost : 0; }
+
 __device__ __forceinline__ void kv_store(const KvLaunch &p, int64_t at, float4 v) {
   if (p.bf16) {
     const __nv_bfloat162 x = __floats2bfloat162_rn(v.x, v.y), y = __floats2bfloat162_rn(v.z, v.w);
@@ -137,176 +158,243 @@ __device__ __forceinline__ int64_t kv_out_at(const KvLaunch &p, int s, int head,
   return ((static_cast<int64_t>(s) * p.a.m + i) * p.a.hq + head * p.ratio + h) * d;
 }
 
+// Four dims of a row, added up over partial results.
+struct KvSum {
+  float m = -INFINITY, l = 0.0f;
+  float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+  __device__ __forceinline__ void add(float m2, float l2, float4 v) {
+    const float next = fmaxf(m, m2), ref = next == -INFINITY ? 0.0f : next;
+    const float keep = exp2_approx(m - ref), k = exp2_approx(m2 - ref);
+    m = next;
+    l = fmaf(l, keep, k * l2);
+    o.x = fmaf(o.x, keep, k * v.x), o.y = fmaf(o.y, keep, k * v.y);
+    o.z = fmaf(o.z, keep, k * v.z), o.w = fmaf(o.w, keep, k * v.w);
+  }
+  __device__ __forceinline__ float4 result() const {
+    const float inv = l > 0.0f ? 1.0f / l : 0.0f;
+    return make_float4(o.x * inv, o.y * inv, o.z * inv, o.w * inv);
+  }
+};
+
 // ---- the kernel -------------------------------------------------------------
 //
-// Work is the line of all groups of all items, an item being (sequence, head,
-// tile of query rows); each block takes an equal run of it, whatever the
-// sequences' lengths, and its warps equal parts of each item's run. A warp
-// brings its groups by bulk copies into a ring of its own and holds the running
-// maximum, sum and outputs of its keys; at an item's end the warps are joined
-// in shared memory. An item that lies in one block is finished there; the
-// others leave partial results, which a second launch joins.
+// Work is a line on which the items, an item being (sequence, head, tile of
+// query rows), lie one after the other, each as long as its groups of keys and
+// what beginning it costs. Every warp takes an equal run of the line, whatever
+// the sequences' lengths, and works alone: it brings its groups by bulk copies
+// into a ring of its own, across the ends of items, and holds the running
+// maximum, sum and outputs of its keys. An item that one warp has whole is
+// finished there; the others' partial results are joined, in the block where
+// the item lies in it, else by a second launch.
 //
 // Products run on the tensor cores with the cached codes as exact fp16
-// integers. Eight query rows fill a 16-row tile: rows 0..7 hold the leading
-// fp16 term and rows 8..15 the remainder (22 bits together), so fp32 accuracy
-// costs no more products than the tile has. A key's block scale multiplies the
-// finished 32-dim dot in fp32; a value's block scale goes into the weight,
-// p d_v, before it is split. Each step's sums are added to fp32 registers
-// outside the tensor core, which does not round its sums to nearest.
-template <int NB, bool KQ8, bool VQ8, int MT>
+// integers. fp32 queries (FINE): eight rows fill a 16-row tile, rows 0..7 with
+// the leading fp16 term and rows 8..15 with the remainder (22 bits together),
+// so fp32 accuracy costs no more products than the tile has. bf16 queries, and
+// the weights that go with them, are one term and fill sixteen rows. A key's
+// block scale multiplies the finished 32-dim dot in fp32; a value's block scale
+// goes into the weight, p d_v, in fp16 with the product's own remainder (FINE).
+// Each step's sums are added to fp32 registers outside the tensor core, which
+// does not round its sums to nearest.
+template <int NB, bool KQ8, bool VQ8, int OCT, bool FINE>
 __device__ __forceinline__ void kv_attn_body(const KvLaunch &p, uint32_t *status) {
-  using C = KvCfg<NB, KQ8, VQ8, MT>;
-  constexpr int NW = C::kNW, TG = C::kTG, S = C::kStages, D = C::kD;
+  using C = KvCfg<NB, KQ8, VQ8, OCT, FINE>;
+  constexpr int NW = C::kNW, TG = C::kTG, S = C::kStages, D = C::kD, MT = C::kMT;
+  constexpr int kThreads = NW * 32;
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ __align__(8) uint64_t bars[NW * S];
-  __shared__ float w_max[NW][8], w_sum[NW][8];
-  __shared__ int64_t scan[NW];
-  __shared__ int start_seq;
-  __shared__ int64_t start_base;
+  __shared__ int64_t scan[kThreads + 1];
+  struct Piece {
+    int seq, head, tile, a, b, n;
+  };
+  __shared__ Piece pieces[2 * NW];
 
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, t = lane & 3;
-  __shared__ float q_factor[C::kRows];
-  uint4 *qfrag = reinterpret_cast<uint4 *>(smem);  // [MT][NB][2][32]
-  const uint32_t qfrag_s = smem_u32(qfrag);
-  float *joins = reinterpret_cast<float *>(smem + C::kQBytes);
-  float *join = joins + warp * 8 * C::kRowPad;
-  uint8_t *ring = smem + C::kQBytes + NW * 8 * C::kRowPad * 4 + warp * S * C::kStageBytes;
+  uint8_t *own = smem + warp * C::warp_bytes(TG, S);
+  uint4 *qfrag = reinterpret_cast<uint4 *>(own);  // [MT][NB][2][32]
+  uint8_t *ring = own + C::kQBytes;
+  const uint32_t qfrag_s = smem_u32(qfrag) + lane * 16, ring_s = smem_u32(ring);
   uint64_t *bar = bars + warp * S;
 
   if (lane == 0) {
     for (int i = 0; i < S; ++i) mbar_init(bar + i, 1);
     fence_mbar_init();
   }
+  if (tid < 2 * NW) pieces[tid].seq = -1;
   pdl_launch_dependents();
   pdl_wait();
 
-  // The line's length and this block's run of it.
+  // The line: scan[i] is where the sequences of thread i begin on it.
   const int64_t per_seq = static_cast<int64_t>(p.f.heads) * p.tiles;
-  const int chunk = (p.a.batch + NW * 32 - 1) / (NW * 32);
-  const int s0 = min(p.a.batch, tid * chunk), s1 = min(p.a.batch, s0 + chunk);
-  int64_t mine = 0;
-  for (int s = s0; s < s1; ++s) mine += kv_seq(p, s, status).n * per_seq;
-  int64_t incl = mine;
-  for (int o = 1; o < 32; o <<= 1) {
-    const int64_t v = __shfl_up_sync(0xffffffffu, incl, o);
-    if (lane >= o) incl += v;
+  const int chunk = (p.a.batch + kThreads - 1) / kThreads;
+  {
+    const int s0 = min(p.a.batch, tid * chunk), s1 = min(p.a.batch, s0 + chunk);
+    int64_t incl = 0;
+    for (int s = s0; s < s1; ++s) {
+      const KvSeq q = kv_seq(p, s, status);
+      incl += kv_units(q.n) * per_seq;
+    }
+    for (int o = 1; o < 32; o <<= 1) {
+      const int64_t v = __shfl_up_sync(0xffffffffu, incl, o);
+      if (lane >= o) incl += v;
+    }
+    scan[tid + 1] = incl;
+    if (tid == 0) scan[0] = 0;
+    __syncthreads();
+    int64_t before = 0;
+    for (int w = 0; w < warp; ++w) before += scan[w * 32 + 32];
+    __syncthreads();
+    scan[tid + 1] = incl + before;
+    __syncthreads();
   }
-  if (lane == 31) scan[warp] = incl;
-  __syncthreads();
-  int64_t total = 0;
-  for (int w = 0; w < NW; ++w) {
-    if (w < warp) incl += scan[w];
-    total += scan[w];
-  }
+  const int64_t total = scan[kThreads];
+
   // Rows of sequences without keys.
   for (int s = blockIdx.x; s < p.a.batch; s += gridDim.x) {
     if (kv_seq(p, s, status).n) continue;
     const int64_t n = static_cast<int64_t>(p.a.m) * p.a.hq * D;
-    for (int64_t e = tid * 4; e < n; e += NW * 128) kv_store(p, s * n + e, make_float4(0.f, 0.f, 0.f, 0.f));
+    for (int64_t e = tid * 4; e < n; e += kThreads * 4) kv_store(p, s * n + e, make_float4(0.f, 0.f, 0.f, 0.f));
   }
-  const int64_t blocks = min(static_cast<int64_t>(gridDim.x), (total + p.min_groups - 1) / p.min_groups);
+
+  // Blocks that work, this block's run of the line, and this warp's part of it.
+  const int64_t least = static_cast<int64_t>(p.min_units) * NW;
+  const int64_t blocks = min(static_cast<int64_t>(gridDim.x), (total + least - 1) / least);
   KvSplit *splits = reinterpret_cast<KvSplit *>(p.a.ws);
-  float *slots = p.a.ws + kKvMaxBlocks * 4;
-  if (blockIdx.x >= blocks) {
-    if (tid == 0) splits[blockIdx.x].seq = -1;
-    return;
-  }
-  int64_t pos = blockIdx.x * total / blocks;
-  const int64_t end = (blockIdx.x + 1) * total / blocks;
-  if (incl - mine <= pos && pos < incl) {
-    int64_t base = incl - mine;
-    int s = s0;
-    for (;; ++s) {
-      const int64_t n = kv_seq(p, s, status).n * per_seq;
-      if (pos < base + n) break;
-      base += n;
-    }
-    start_seq = s;
-    start_base = base;
-  }
-  __syncthreads();
-  int seq = start_seq;
-  int64_t base = start_base;
+  constexpr int64_t kSlot = kv_attn_slot_floats(C::kRows, D);
+  float *block_slots = p.a.ws + kKvMaxBlocks * 4 + 2 * blockIdx.x * kSlot;
+  float *warp_slots = p.a.ws + kKvMaxBlocks * (4 + 2 * kSlot) + 2 * NW * blockIdx.x * kSlot;
+  if (tid == 0) splits[blockIdx.x].seq = -1;
+  if (blockIdx.x >= blocks) return;
+  const int64_t from = blockIdx.x * total / blocks, span = (blockIdx.x + 1) * total / blocks - from;
 
-  // The item at `pos`, and this warp's groups of it.
-  struct Run {
-    int seq, head, tile, len, n, a, b;  // item's groups [a, b) of n; a group's number counts from the sequence's first
-    int lo, hi;                         // this warp's groups, numbered in the sequence
-  } run, next;
-  auto locate = [&](Run &r) {
-    KvSeq q = kv_seq(p, seq, status);
-    while (pos >= base + q.n * per_seq) {
-      base += q.n * per_seq;
-      q = kv_seq(p, ++seq, status);
-    }
-    const int64_t in = pos - base;
-    const int item = static_cast<int>(in / q.n);
-    r.seq = seq;
-    r.head = item / p.tiles;
-    r.tile = item - r.head * p.tiles;
-    r.len = q.len;
-    r.n = q.n;
-    r.a = static_cast<int>(in - static_cast<int64_t>(item) * q.n);
-    r.b = static_cast<int>(min(static_cast<int64_t>(q.n), r.a + (end - pos)));
-    const int ng = r.b - r.a;
-    r.lo = q.first + r.a + static_cast<int>(static_cast<int64_t>(ng) * warp / NW);
-    r.hi = q.first + r.a + static_cast<int>(static_cast<int64_t>(ng) * (warp + 1) / NW);
+  // A warp's place on the line: an item's groups [a, b) of n, and the units behind them.
+  struct Place {
+    int seq, head, tile, len, first, n, a, b;
+    int64_t left;
   };
-
-  const int per_page = p.f.page / kKvGroup;
-  const int page_shift = 31 - __clz(per_page);
-  const uint64_t policy = l2_evict_first_policy();
-  const uint32_t ring_s = smem_u32(ring);
-  uint32_t put = 0, got = 0;  // stages filled and used so far (ring positions)
-  uint32_t ok_bits = 0;       // groups of the ring whose page exists
-  bool dead = false;          // a wait ran out
-
-  // Fill the ring's next stage with the step of groups [grp, grp + TG) of `r`.
-  auto fill = [&](const Run &r, int grp) {
-    const int st = put % S;
-    uint32_t ok = 0;
-    const int32_t *table = p.a.table + r.seq * p.a.table_stride;
-    int64_t page[TG];
-#pragma unroll
-    for (int i = 0; i < TG; ++i) {
-      page[i] = -1;
-      if (grp + i < r.hi) {
-        page[i] = __ldg(table + ((grp + i) >> page_shift));
-        if (page[i] < 0 || page[i] >= p.f.pages) {
-          page[i] = -1;
-          if (lane == 0) atomicOr(status, kDevBadIndex);
+  // The part of the item at hand that begins `skip` units into it.
+  auto enter = [&](Place &c, int64_t skip) {
+    const int64_t a = max(skip - kKvItemCost, int64_t(0));
+    const int64_t b = min(static_cast<int64_t>(c.n), max(skip + c.left - kKvItemCost, int64_t(0)));
+    c.a = static_cast<int>(a);
+    c.b = static_cast<int>(b);
+    c.left -= min(kv_units(c.n) - skip, c.left);
+  };
+  auto look = [&](Place &c) {
+    const KvSeq q = kv_seq(p, c.seq, status);
+    c.len = q.len, c.first = q.first, c.n = q.n;
+  };
+  // The next item with groups for this warp; c.b == c.a at the end.
+  auto next = [&](Place &c) {
+    c.a = c.b = 0;
+    while (c.left > 0 && c.b == c.a) {
+      if (++c.tile == p.tiles) {
+        c.tile = 0;
+        if (++c.head == p.f.heads) {
+          c.head = 0;
+          do {
+            if (++c.seq >= p.a.batch) {
+              c.left = 0;
+              return;
+            }
+            look(c);
+          } while (c.n == 0);
         }
       }
-      if (page[i] >= 0) ok |= 1u << i;
+      enter(c, 0);
     }
-    if (lane == 0) {
-      mbar_arrive_expect_tx(bar + st, __popc(ok) * C::kGroupBytes);
-#pragma unroll
-      for (int i = 0; i < TG; ++i)
-        if (page[i] >= 0)
-          bulk_g2s(ring + st * C::kStageBytes + i * C::kGroupBytes,
-                   p.a.cache + ((page[i] * p.f.heads + r.head) * per_page + ((grp + i) & (per_page - 1))) *
-                                   static_cast<int64_t>(C::kGroupBytes),
-                   C::kGroupBytes, bar + st, policy);
+  };
+  Place use{};
+  {
+    const int64_t pos = from + span * warp / NW;
+    use.left = from + span * (warp + 1) / NW - pos;
+    if (use.left > 0) {
+      int lo = 0, hi = kThreads;  // scan[lo] <= pos < scan[hi]
+      while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if (scan[mid] <= pos)
+          lo = mid;
+        else
+          hi = mid;
+      }
+      int64_t base = scan[lo];
+      use.seq = lo * chunk;
+      look(use);
+      while (pos >= base + kv_units(use.n) * per_seq) {
+        base += kv_units(use.n) * per_seq;
+        ++use.seq;
+        look(use);
+      }
+      const int64_t units = kv_units(use.n);
+      const int item = static_cast<int>((pos - base) / units);
+      use.head = item / p.tiles;
+      use.tile = item - use.head * p.tiles;
+      enter(use, pos - base - item * units);
+      if (use.a == use.b) next(use);
     }
+  }
+
+  const int per_page = p.f.page / kKvGroup, page_shift = 31 - __clz(per_page);
+  const uint64_t policy = l2_evict_first_policy();
+  Place put = use;
+  int put_grp = put.first + put.a;
+  uint32_t filled = 0, used = 0;  // stages of the ring so far
+  uint32_t ok_bits = 0;           // groups in the ring whose page exists
+  bool dead = false;              // a wait ran out
+
+  // Fill the ring's next stage with the next step of TG groups, one lane a group.
+  auto fill = [&]() {
+    if (put.a == put.b) return;
+    const int st = filled % S;
+    const int grp = put_grp + lane, end = put.first + put.b;
+    int page = -1;
+    if (lane < TG && grp < end) {
+      page = __ldg(p.a.table + put.seq * p.a.table_stride + (grp >> page_shift));
+      if (page < 0 || page >= p.f.pages) {
+        page = -1;
+        atomicOr(status, kDevBadIndex);
+      }
+    }
+    const uint32_t ok = __ballot_sync(0xffffffffu, page >= 0);
+    if (lane == 0) mbar_arrive_expect_tx(bar + st, __popc(ok) * C::kGroupBytes);
+    __syncwarp();
+    if (page >= 0)
+      bulk_g2s(ring + st * C::kStageBytes + lane * C::kGroupBytes,
+               p.a.cache + ((static_cast<int64_t>(page) * p.f.heads + put.head) * per_page + (grp & (per_page - 1))) *
+                               C::kGroupBytes,
+               C::kGroupBytes, bar + st, policy);
     ok_bits = (ok_bits & ~(((1u << TG) - 1) << (st * TG))) | ok << (st * TG);
-    ++put;
+    ++filled;
+    put_grp += TG;
+    if (put_grp >= end) {
+      next(put);
+      put_grp = put.first + put.a;
+    }
   };
 
-  // Query rows of `r` as fragments, each row brought to [2^14, 2^15) by a power
-  // of two so that both terms stay in fp16's range; its inverse, with the
-  // softmax's scale and log2(e), is the factor of the row's scores. Warp w
-  // makes the fragments of units (tile, block) w, w + NW, ...
-  auto load_q = [&](const Run &r) {
-    for (int u = warp; u < MT * NB; u += NW) {
-      const int mt = u / NB, mine_b = u - mt * NB;
-      const int row = r.tile * C::kRows + mt * 8 + g;
+  for (int i = 0; i < S; ++i) fill();
+
+  while (use.a < use.b && !dead) {
+    float top[OCT], sum[OCT];  // of rows 8 o + g
+    float2 acc[OCT][NB * 4];
+    int last[OCT], low[OCT];
+    float factor[OCT];
+
+    // ---- query rows as fragments ----
+    // Each row is brought to [2^14, 2^15) by a power of two so that both terms
+    // stay in fp16's range; its inverse, with the softmax's scale and log2(e),
+    // is the factor of the row's scores, positive: the scale's sign goes into
+    // the row.
+    __syncwarp();
+#pragma unroll
+    for (int o = 0; o < OCT; ++o) {
+      const int row = use.tile * C::kRows + o * 8 + g;
       const bool there = row < p.rows;
-      const int i = there ? row / p.ratio : 0, h = there ? row - i * p.ratio : 0;
-      const int64_t at = r.seq * p.a.q_seq + i * p.a.q_tok +
-                         (static_cast<int64_t>(r.head) * p.ratio + h) * p.a.q_head + 4 * t;
-      float x[8], top = 0.0f;
+      const int i = min(row / p.ratio, p.a.m - 1), h = there ? row - i * p.ratio : 0;
+      const int64_t at = use.seq * p.a.q_seq + i * p.a.q_tok +
+                         (static_cast<int64_t>(use.head) * p.ratio + h) * p.a.q_head + 4 * t;
+      float4 x[NB][2];
+      float big = 0.0f;
 #pragma unroll
       for (int b = 0; b < NB; ++b)
 #pragma unroll
@@ -314,163 +402,160 @@ __device__ __forceinline__ void kv_attn_body(const KvLaunch &p, uint32_t *status
           const int64_t e = at + b * 32 + half * 16;
           float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
           if (there) {
-            if (p.bf16) {
+            if (FINE) {
+              v = *reinterpret_cast<const float4 *>(static_cast<const float *>(p.a.q) + e);
+            } else {
               const uint2 w = *reinterpret_cast<const uint2 *>(static_cast<const __nv_bfloat16 *>(p.a.q) + e);
               v = make_float4(__uint_as_float(w.x << 16), __uint_as_float(w.x & 0xffff0000u),
                               __uint_as_float(w.y << 16), __uint_as_float(w.y & 0xffff0000u));
-            } else {
-              v = *reinterpret_cast<const float4 *>(static_cast<const float *>(p.a.q) + e);
             }
           }
-          top = fmaxf(top, fmaxf(fmaxf(fabsf(v.x), fabsf(v.y)), fmaxf(fabsf(v.z), fabsf(v.w))));
-          if (b == mine_b) x[half * 4] = v.x, x[half * 4 + 1] = v.y, x[half * 4 + 2] = v.z, x[half * 4 + 3] = v.w;
+          big = fmaxf(big, fmaxf(fmaxf(fabsf(v.x), fabsf(v.y)), fmaxf(fabsf(v.z), fabsf(v.w))));
+          x[b][half] = v;
         }
-      top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
-      top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
-      // exponent of top, at least -100 (smaller rows keep fewer bits of scores that are 0 anyway)
-      const int ex = max(static_cast<int>(__float_as_uint(top) >> 23) - 127, -100);
-      const float up = __uint_as_float(static_cast<uint32_t>(14 - ex + 127) << 23);
-      if (mine_b == 0 && t == 0)
-        q_factor[mt * 8 + g] = p.a.scale * 1.44269504088896f * __uint_as_float(static_cast<uint32_t>(ex - 14 + 127) << 23);
+      big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, 1));
+      big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, 2));
+      // exponent of the largest, at least -100 (smaller rows keep fewer bits of scores that are 0 anyway)
+      const int ex = max(static_cast<int>(__float_as_uint(big) >> 23) - 127, -100);
+      float up = __uint_as_float(static_cast<uint32_t>(14 - ex + 127) << 23);
+      factor[o] = p.a.scale == 0.0f ? 1.0f
+                                    : fabsf(p.a.scale) * 1.44269504088896f *
+                                          __uint_as_float(static_cast<uint32_t>(ex - 14 + 127) << 23);
+      if (p.a.scale <= 0.0f) up = p.a.scale < 0.0f ? -up : 0.0f;
 #pragma unroll
-      for (int half = 0; half < 2; ++half) {
-        uint4 f;
-        split_f16(x[half * 4] * up, x[half * 4 + 2] * up, f.x, f.y);
-        split_f16(x[half * 4 + 1] * up, x[half * 4 + 3] * up, f.z, f.w);
-        qfrag[(u * 2 + half) * 32 + lane] = f;
-      }
+      for (int b = 0; b < NB; ++b)
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {
+          const float4 v = x[b][half];
+          const float2 even = make_float2(v.x * up, v.z * up), odd = make_float2(v.y * up, v.w * up);
+          uint32_t *f = reinterpret_cast<uint32_t *>(qfrag + (((FINE ? o : o / 2) * NB + b) * 2 + half) * 32 + lane);
+          if (FINE) {
+            __half2 h0, l0, h1, l1;
+            split_f16(even, h0, l0);
+            split_f16(odd, h1, l1);
+            *reinterpret_cast<uint4 *>(f) = make_uint4(h2_bits(h0), h2_bits(l0), h2_bits(h1), h2_bits(l1));
+          } else {
+            f[o & 1] = h2_bits(__float22half2_rn(even));
+            f[2 + (o & 1)] = h2_bits(__float22half2_rn(odd));
+            if (OCT == 1) f[1] = f[3] = 0u;
+          }
+        }
+      top[o] = -INFINITY;
+      sum[o] = 0.0f;
+#pragma unroll
+      for (int n = 0; n < NB * 4; ++n) acc[o][n] = make_float2(0.0f, 0.0f);
+      last[o] = use.len - p.a.m + i;
+      low[o] = p.a.window > 0 ? max(0, last[o] - p.a.window + 1) : 0;
     }
-  };
+    __syncwarp();
+    const int low_all = p.a.window > 0 ? max(0, use.len - p.a.m - p.a.window + 1) : 0;
+    const int grp_end = use.first + use.b;
+    int up_exp = 13;  // acc and sum are 2^up_exp and 2^13 times the outputs' and weights' sums
 
-  locate(run);
-  for (int i = 0; i < S; ++i)
-    if (run.lo + i * TG < run.hi) fill(run, run.lo + i * TG);
-  load_q(run);
-  __syncthreads();
-
-  while (true) {
-    // ---- this warp's groups of the item ----
-    float top[MT], sum[MT], acc[MT][NB * 4][2];
-    int last[MT], low[MT];
-    float factor[MT];
-#pragma unroll
-    for (int mt = 0; mt < MT; ++mt) {
-      top[mt] = -INFINITY;
-      sum[mt] = 0.0f;
-#pragma unroll
-      for (int n = 0; n < NB * 4; ++n) acc[mt][n][0] = acc[mt][n][1] = 0.0f;
-      const int i = min((run.tile * C::kRows + mt * 8 + g) / p.ratio, p.a.m - 1);
-      last[mt] = run.len - p.a.m + i;
-      low[mt] = p.a.window > 0 ? max(0, last[mt] - p.a.window + 1) : 0;
-      factor[mt] = q_factor[mt * 8 + g];
-    }
-    const int low_all = p.a.window > 0 ? max(0, run.len - p.a.m - p.a.window + 1) : 0;
-    int up_exp = 0;  // acc is 2^up_exp times the outputs' sums
-
-    for (int grp = run.lo; grp < run.hi; grp += TG) {
-      const int st = got % S;
-      if (!dead && !mbar_wait(bar + st, (got / S) & 1)) {
+    for (int grp = use.first + use.a; grp < grp_end; grp += TG) {
+      const int st = used % S;
+      if (!__all_sync(0xffffffffu, mbar_wait(bar + st, (used / S) & 1))) {
         // Nothing more is copied; what is in flight is waited for once more.
         bool drained = true;
-        for (uint32_t i = got; i != put; ++i) drained = mbar_wait(bar + i % S, (i / S) & 1) && drained;
+        for (uint32_t i = used; i != filled; ++i) drained = mbar_wait(bar + i % S, (i / S) & 1) && drained;
         if (lane == 0) atomicOr(status, kDevTimeoutFull | (drained ? 0u : kDevTimeoutDrain));
         dead = true;
+        break;
       }
-      ++got;
-      if (dead) continue;
+      ++used;
       const uint32_t stage = ring_s + st * C::kStageBytes;
       const uint32_t ok = ok_bits >> (st * TG) & ((1u << TG) - 1);
       const int key0 = grp * kKvGroup;
-      const bool full = ok == (1u << TG) - 1 && key0 + TG * kKvGroup <= run.len - p.a.m + 1 &&
-                        (p.a.window == 0 || key0 >= run.len - p.a.window);
+      const bool full = ok == (1u << TG) - 1 && key0 + TG * kKvGroup <= use.len - p.a.m + 1 &&
+                        (p.a.window == 0 || key0 >= use.len - p.a.window);
 
       // ---- scores ----
-      float z[MT][TG][2][2];
-      {
-        constexpr int KW = KQ8 ? 2 * NB : NB;
-        uint32_t kw[TG][2][KW];
-        uint32_t ks[TG][NB][2];
+      float2 z[OCT][TG][2];
 #pragma unroll
-        for (int gi = 0; gi < TG; ++gi) {
-          const uint32_t part = stage + gi * C::kGroupBytes;
+      for (int o = 0; o < OCT; ++o)
+#pragma unroll
+        for (int gi = 0; gi < TG; ++gi) z[o][gi][0] = z[o][gi][1] = make_float2(0.0f, 0.0f);
+#pragma unroll
+      for (int first = 0; first < NB;) {
+        const int n = kv_run(NB, KQ8, first).n, bytes = n * (KQ8 ? 8 : 4);
+        uint32_t kw[TG][2][4];
+#pragma unroll
+        for (int gi = 0; gi < TG; ++gi)
 #pragma unroll
           for (int j = 0; j < 2; ++j) {
-#pragma unroll
-            for (int first = 0; first < NB;) {
-              const int n = kv_run(NB, KQ8, first).n, bytes = n * (KQ8 ? 8 : 4), w0 = first * (KQ8 ? 2 : 1);
-              const uint32_t at = part + first * (KQ8 ? 512 : 256) + (j * 32 + lane) * bytes;
-              if (bytes == 16) {
-                const uint4 v = lds_u4(at);
-                kw[gi][j][w0] = v.x, kw[gi][j][w0 + 1] = v.y, kw[gi][j][w0 + 2] = v.z, kw[gi][j][w0 + 3] = v.w;
-              } else if (bytes == 8) {
-                const uint2 v = lds_u2(at);
-                kw[gi][j][w0] = v.x, kw[gi][j][w0 + 1] = v.y;
-              } else {
-                kw[gi][j][w0] = lds_u32(at);
-              }
-              first += n;
+            const uint32_t at = stage + gi * C::kGroupBytes + first * (KQ8 ? 512 : 256) + (j * 32 + lane) * bytes;
+            if (bytes == 16) {
+              const uint4 v = lds_u4(at);
+              kw[gi][j][0] = v.x, kw[gi][j][1] = v.y, kw[gi][j][2] = v.z, kw[gi][j][3] = v.w;
+            } else if (bytes == 8) {
+              const uint2 v = lds_u2(at);
+              kw[gi][j][0] = v.x, kw[gi][j][1] = v.y;
+            } else {
+              kw[gi][j][0] = lds_u32(at);
             }
           }
 #pragma unroll
-          for (int b = 0; b < NB; ++b) {
-            const uint2 v = lds_u2(part + kv_code_bytes(NB, KQ8) + (t * NB + b) * 8);
-            ks[gi][b][0] = v.x, ks[gi][b][1] = v.y;
-          }
-        }
-#pragma unroll
-        for (int mt = 0; mt < MT; ++mt)
-#pragma unroll
-          for (int gi = 0; gi < TG; ++gi) z[mt][gi][0][0] = z[mt][gi][0][1] = z[mt][gi][1][0] = z[mt][gi][1][1] = 0.0f;
-#pragma unroll
-        for (int b = 0; b < NB; ++b) {
+        for (int r = 0; r < n; ++r) {
+          const int b = first + r;
           uint4 qa[MT][2];
 #pragma unroll
           for (int mt = 0; mt < MT; ++mt) {
-            qa[mt][0] = lds_u4(qfrag_s + (((mt * NB + b) * 2) * 32 + lane) * 16);
-            qa[mt][1] = lds_u4(qfrag_s + (((mt * NB + b) * 2 + 1) * 32 + lane) * 16);
+            qa[mt][0] = lds_u4(qfrag_s + (mt * NB + b) * 1024);
+            qa[mt][1] = lds_u4(qfrag_s + (mt * NB + b) * 1024 + 512);
           }
 #pragma unroll
-          for (int gi = 0; gi < TG; ++gi)
+          for (int gi = 0; gi < TG; ++gi) {
+            const uint2 ks = lds_u2(stage + gi * C::kGroupBytes + kv_code_bytes(NB, KQ8) + (t * NB + b) * 8);
 #pragma unroll
             for (int j = 0; j < 2; ++j) {
               uint32_t k00, k01, k10, k11;
               if (KQ8) {
-                const uint32_t w0 = kw[gi][j][KQ8 ? 2 * b : b] ^ 0x80808080u;
-                const uint32_t w1 = kw[gi][j][KQ8 ? 2 * b + 1 : b] ^ 0x80808080u;
+                const uint32_t w0 = kw[gi][j][(2 * r) & 3] ^ 0x80808080u, w1 = kw[gi][j][(2 * r + 1) & 3] ^ 0x80808080u;
                 k00 = q8_pair<0x4240>(w0), k01 = q8_pair<0x4341>(w0);
                 k10 = q8_pair<0x4240>(w1), k11 = q8_pair<0x4341>(w1);
               } else {
-                const uint32_t w = kw[gi][j][b], w8 = w >> 8;
+                const uint32_t w = kw[gi][j][r], w8 = w >> 8;
                 k00 = q4_low(w), k01 = q4_low(w8), k10 = q4_high(w), k11 = q4_high(w8);
               }
-              const float2 d = __half22float2(bits_h2(ks[gi][b][j]));
+              const float2 d = __half22float2(bits_h2(j ? ks.y : ks.x));
 #pragma unroll
               for (int mt = 0; mt < MT; ++mt) {
-                float c[4] = {0.f, 0.f, 0.f, 0.f};
-                mma_f16(c, qa[mt][0], k00, k01);
-                mma_f16(c, qa[mt][1], k10, k11);
-                z[mt][gi][j][0] = fmaf(d.x, c[0] + c[2], z[mt][gi][j][0]);
-                z[mt][gi][j][1] = fmaf(d.y, c[1] + c[3], z[mt][gi][j][1]);
+                const float4 c = mma_f16(qa[mt][1], k10, k11,
+                                         mma_f16(qa[mt][0], k00, k01, make_float4(0.f, 0.f, 0.f, 0.f)));
+                const float2 upper = make_float2(c.x, c.y), lower = make_float2(c.z, c.w);
+                if (FINE) {
+                  z[mt][gi][j] = __ffma2_rn(d, __fadd2_rn(upper, lower), z[mt][gi][j]);
+                } else {
+                  z[2 * mt][gi][j] = __ffma2_rn(d, upper, z[2 * mt][gi][j]);
+                  if (OCT > 1) z[min(2 * mt + 1, OCT - 1)][gi][j] = __ffma2_rn(d, lower, z[min(2 * mt + 1, OCT - 1)][gi][j]);
+                }
               }
             }
+          }
         }
+        first += n;
       }
-#pragma unroll
-      for (int mt = 0; mt < MT; ++mt)
-#pragma unroll
-        for (int gi = 0; gi < TG; ++gi)
-#pragma unroll
-          for (int e = 0; e < 4; ++e) z[mt][gi][e >> 1][e & 1] *= factor[mt];
 
       // ---- scales of the values, and what the masks leave ----
       uint32_t vs[TG][NB][2];
 #pragma unroll
-      for (int gi = 0; gi < TG; ++gi)
+      for (int gi = 0; gi < TG; ++gi) {
+        const uint32_t at = stage + gi * C::kGroupBytes + C::kKeyPart + kv_code_bytes(NB, VQ8) + t * NB * 8;
 #pragma unroll
-        for (int b = 0; b < NB; ++b) {
-          const uint2 v = lds_u2(stage + gi * C::kGroupBytes + C::kKeyPart + kv_code_bytes(NB, VQ8) + (t * NB + b) * 8);
-          vs[gi][b][0] = v.x, vs[gi][b][1] = v.y;
+        for (int b = 0; b < NB; b += 2) {
+          if (NB % 2 == 0) {
+            const uint4 v = lds_u4(at + b * 8);
+            vs[gi][b][0] = v.x, vs[gi][b][1] = v.y, vs[gi][min(b + 1, NB - 1)][0] = v.z, vs[gi][min(b + 1, NB - 1)][1] = v.w;
+          } else {
+            const uint2 v = lds_u2(at + b * 8);
+            vs[gi][b][0] = v.x, vs[gi][b][1] = v.y;
+            if (b + 1 < NB) {
+              const uint2 u = lds_u2(at + b * 8 + 8);
+              vs[gi][min(b + 1, NB - 1)][0] = u.x, vs[gi][min(b + 1, NB - 1)][1] = u.y;
+            }
+          }
         }
+      }
       if (!full) {
 #pragma unroll
         for (int gi = 0; gi < TG; ++gi) {
@@ -479,81 +564,97 @@ __device__ __forceinline__ void kv_attn_body(const KvLaunch &p, uint32_t *status
           for (int e = 0; e < 4; ++e) {  // e = tok / 4: column e & 1 of half e >> 1
             const int key = key0 + gi * kKvGroup + t + 4 * e;
 #pragma unroll
-            for (int mt = 0; mt < MT; ++mt)
-              if (!there || key > last[mt] || key < low[mt]) z[mt][gi][e >> 1][e & 1] = -INFINITY;
+            for (int o = 0; o < OCT; ++o)
+              if (!there || key > last[o] || key < low[o]) (e & 1 ? z[o][gi][e >> 1].y : z[o][gi][e >> 1].x) = -INFINITY;
             // what no row sees may be anything, NaN among it: its scale is 0
-            if (!there || key >= run.len || key < low_all)
+            if (!there || key >= use.len || key < low_all)
 #pragma unroll
               for (int b = 0; b < NB; ++b) vs[gi][b][e >> 1] &= e & 1 ? 0x0000ffffu : 0xffff0000u;
           }
         }
       }
-
-      // ---- running maximum and sum ----
-      float keep[MT];
-#pragma unroll
-      for (int mt = 0; mt < MT; ++mt) {
-        float m = -INFINITY;
-#pragma unroll
-        for (int gi = 0; gi < TG; ++gi)
-          m = fmaxf(m, fmaxf(fmaxf(z[mt][gi][0][0], z[mt][gi][0][1]), fmaxf(z[mt][gi][1][0], z[mt][gi][1][1])));
-        m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 1));
-        m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 2));
-        m = fmaxf(m, top[mt]);
-        const float ref = m == -INFINITY ? 0.0f : m;
-        keep[mt] = exp2_approx(top[mt] - ref);
-        top[mt] = m;
-        float add = 0.0f;
-#pragma unroll
-        for (int gi = 0; gi < TG; ++gi)
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const float w = exp2_approx(z[mt][gi][e >> 1][e & 1] - ref);
-            z[mt][gi][e >> 1][e & 1] = w;
-            add += w;
-          }
-        sum[mt] = fmaf(sum[mt], keep[mt], add);
-      }
-
-      // ---- outputs ----
-      // A power of two brings the largest weight p d_v of the step below 2^15,
-      // so that the split keeps its 22 bits however small the values are.
-      uint32_t big = 0;
+      // The weights are p 2^13 and so p d_v 2^13: inside fp16 with room for both
+      // terms while the largest scale is in [2^-7, 2). Outside, the scales of the
+      // step are brought there by a power of two, which the sums keep (up_exp).
+      uint32_t bits = 0;
 #pragma unroll
       for (int gi = 0; gi < TG; ++gi)
 #pragma unroll
-        for (int b = 0; b < NB; ++b)
-          big = __vmaxu2(big, __vmaxu2(vs[gi][b][0] & 0x7fff7fffu, vs[gi][b][1] & 0x7fff7fffu));
-      big = __reduce_max_sync(0xffffffffu, max(big & 0xffffu, big >> 16));
-      const int e_new = 29 - static_cast<int>(max(big >> 10, 1u));
-      const float up = __uint_as_float(static_cast<uint32_t>(e_new + 127) << 23);
-      const float turn = __uint_as_float(static_cast<uint32_t>(e_new - up_exp + 127) << 23);
-      up_exp = e_new;
-#pragma unroll
-      for (int mt = 0; mt < MT; ++mt) {
-        keep[mt] *= turn;
+        for (int b = 0; b < NB; ++b) bits |= vs[gi][b][0] | vs[gi][b][1];
+      bits = __reduce_or_sync(0xffffffffu, bits & 0x60006000u);
+      int e_new = 13;
+      if (((bits | bits >> 16) & 0x6000u) != 0x2000u) {
+        uint32_t big = 0;
 #pragma unroll
         for (int gi = 0; gi < TG; ++gi)
 #pragma unroll
-          for (int e = 0; e < 4; ++e) z[mt][gi][e >> 1][e & 1] *= up;
+          for (int b = 0; b < NB; ++b)
+            big = __vmaxu2(big, __vmaxu2(vs[gi][b][0] & 0x7fff7fffu, vs[gi][b][1] & 0x7fff7fffu));
+        big = __reduce_max_sync(0xffffffffu, max(big & 0xffffu, big >> 16));
+        const int by = 14 - static_cast<int>(max(big >> 10, 1u));  // -17 .. 13: two factors of fp16
+        e_new += by;
+        const int by1 = by / 2, by2 = by - by1;
+        const uint32_t f1 = static_cast<uint32_t>(by1 + 15) << 10, f2 = static_cast<uint32_t>(by2 + 15) << 10;
+#pragma unroll
+        for (int gi = 0; gi < TG; ++gi)
+#pragma unroll
+          for (int b = 0; b < NB; ++b)
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+              vs[gi][b][h] = h2_bits(__hmul2(__hmul2(bits_h2(vs[gi][b][h]), bits_h2(f1 | f1 << 16)), bits_h2(f2 | f2 << 16)));
       }
+
+      // ---- running maximum and sum ----
+      float keep[OCT];
+      __half2 ph[OCT][TG][2], pl[FINE ? OCT : 1][TG][2];
+      const float turn = __uint_as_float(static_cast<uint32_t>(e_new - up_exp + 127) << 23);
+      up_exp = e_new;
+#pragma unroll
+      for (int o = 0; o < OCT; ++o) {
+        float m = -INFINITY;
+#pragma unroll
+        for (int gi = 0; gi < TG; ++gi)
+          m = fmaxf(m, fmaxf(fmaxf(z[o][gi][0].x, z[o][gi][0].y), fmaxf(z[o][gi][1].x, z[o][gi][1].y)));
+        m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 1));
+        m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 2));
+        m = fmaxf(m * factor[o], top[o]);
+        const float ref = m == -INFINITY ? 0.0f : m, from13 = 13.0f - ref;
+        const float k = exp2_approx(top[o] - ref);
+        top[o] = m;
+        float2 add = make_float2(0.0f, 0.0f);
+#pragma unroll
+        for (int gi = 0; gi < TG; ++gi)
+#pragma unroll
+          for (int j = 0; j < 2; ++j) {
+            float2 w = __ffma2_rn(z[o][gi][j], make_float2(factor[o], factor[o]), make_float2(from13, from13));
+            w = make_float2(exp2_approx(w.x), exp2_approx(w.y));
+            add = __fadd2_rn(add, w);
+            if (FINE)
+              split_f16(w, ph[o][gi][j], pl[FINE ? o : 0][gi][j]);
+            else
+              ph[o][gi][j] = __float22half2_rn(w);
+          }
+        sum[o] = fmaf(sum[o], k, add.x + add.y);
+        keep[o] = k * turn;
+      }
+
+      // ---- outputs ----
 #pragma unroll
       for (int first = 0; first < NB;) {
-        const int n = kv_run(NB, VQ8, first).n, unit = VQ8 ? 4 : 2, bytes = n * unit;
+        const int n = kv_run(NB, VQ8, first).n, wide = VQ8 ? 4 : 2, bytes = n * wide;
         uint32_t vw[TG][4][2];
 #pragma unroll
         for (int gi = 0; gi < TG; ++gi)
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
-            const int tok4 = e * 4;
-            const uint32_t part = stage + gi * C::kGroupBytes + C::kKeyPart + first * 64 * unit * 2;
+            const uint32_t part = stage + gi * C::kGroupBytes + C::kKeyPart + first * 128 * wide;
             if (bytes == 8) {
-              const uint2 v = lds_u2(part + ((g >> 2) * 64 + (t + tok4) * 4 + (g & 3)) * 8);
+              const uint2 v = lds_u2(part + ((g >> 2) * 64 + t * 4 + (g & 3)) * 8 + e * 128);
               vw[gi][e][0] = v.x, vw[gi][e][1] = v.y;
             } else if (bytes == 4) {
-              vw[gi][e][0] = lds_u32(part + ((t + tok4) * 8 + g) * 4);
+              vw[gi][e][0] = lds_u32(part + (t * 8 + g) * 4 + e * 128);
             } else {
-              vw[gi][e][0] = lds_u16(part + ((t + tok4) * 8 + g) * 2);
+              vw[gi][e][0] = lds_u16(part + (t * 8 + g) * 2 + e * 64);
             }
           }
 #pragma unroll
@@ -566,7 +667,7 @@ __device__ __forceinline__ void kv_attn_body(const KvLaunch &p, uint32_t *status
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
               if (VQ8) {
-                const uint32_t w0 = vw[gi][2 * h][r] ^ 0x80808080u, w1 = vw[gi][2 * h + 1][r] ^ 0x80808080u;
+                const uint32_t w0 = vw[gi][2 * h][r & 1] ^ 0x80808080u, w1 = vw[gi][2 * h + 1][r & 1] ^ 0x80808080u;
                 const uint32_t x = __byte_perm(w0, w1, 0x5140), y = __byte_perm(w0, w1, 0x7362);
                 vb[gi][0][h] = q8_pair<0x4140>(x), vb[gi][2][h] = q8_pair<0x4342>(x);
                 vb[gi][1][h] = q8_pair<0x4140>(y), vb[gi][3][h] = q8_pair<0x4342>(y);
@@ -579,151 +680,175 @@ __device__ __forceinline__ void kv_attn_body(const KvLaunch &p, uint32_t *status
             }
 #pragma unroll
           for (int mt = 0; mt < MT; ++mt) {
-            float c[4][4];
+            float4 c[4];
 #pragma unroll
-            for (int n4 = 0; n4 < 4; ++n4) c[n4][0] = c[n4][1] = c[n4][2] = c[n4][3] = 0.0f;
+            for (int n4 = 0; n4 < 4; ++n4) c[n4] = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
             for (int gi = 0; gi < TG; ++gi) {
-              const float2 d0 = __half22float2(bits_h2(vs[gi][b][0])), d1 = __half22float2(bits_h2(vs[gi][b][1]));
               uint4 w;
-              split_f16(z[mt][gi][0][0] * d0.x, z[mt][gi][0][1] * d0.y, w.x, w.y);
-              split_f16(z[mt][gi][1][0] * d1.x, z[mt][gi][1][1] * d1.y, w.z, w.w);
 #pragma unroll
-              for (int n4 = 0; n4 < 4; ++n4) mma_f16(c[n4], w, vb[gi][n4][0], vb[gi][n4][1]);
+              for (int j = 0; j < 2; ++j) {
+                const __half2 d = bits_h2(vs[gi][b][j]);
+                uint32_t &upper = j ? w.z : w.x, &lower = j ? w.w : w.y;
+                if (FINE) {  // p d_v = hi + what hi leaves of ph d_v + pl d_v
+                  const __half2 hi = __hmul2(ph[mt][gi][j], d);
+                  upper = h2_bits(hi);
+                  lower = h2_bits(__hfma2(pl[FINE ? mt : 0][gi][j], d, __hfma2(ph[mt][gi][j], d, __hneg2(hi))));
+                } else {
+                  upper = h2_bits(__hmul2(ph[2 * mt % OCT][gi][j], d));
+                  lower = OCT == 1 ? 0u : h2_bits(__hmul2(ph[min(2 * mt + 1, OCT - 1)][gi][j], d));
+                }
+              }
+#pragma unroll
+              for (int n4 = 0; n4 < 4; ++n4) c[n4] = mma_f16(w, vb[gi][n4][0], vb[gi][n4][1], c[n4]);
             }
 #pragma unroll
             for (int n4 = 0; n4 < 4; ++n4) {
-              acc[mt][b * 4 + n4][0] = fmaf(acc[mt][b * 4 + n4][0], keep[mt], c[n4][0] + c[n4][2]);
-              acc[mt][b * 4 + n4][1] = fmaf(acc[mt][b * 4 + n4][1], keep[mt], c[n4][1] + c[n4][3]);
+              const float2 upper = make_float2(c[n4].x, c[n4].y), lower = make_float2(c[n4].z, c[n4].w);
+              const int i = b * 4 + n4, o = FINE ? mt : 2 * mt;
+              acc[o][i] = __ffma2_rn(acc[o][i], make_float2(keep[o], keep[o]), FINE ? __fadd2_rn(upper, lower) : upper);
+              if (!FINE && OCT > 1) {
+                const int q = min(o + 1, OCT - 1);
+                acc[q][i] = __ffma2_rn(acc[q][i], make_float2(keep[q], keep[q]), lower);
+              }
             }
           }
         }
         first += n;
       }
       __syncwarp();  // every lane has read the stage
-      if (grp + S * TG < run.hi) fill(run, grp + S * TG);
+      fill();
     }
+    if (dead) break;
 
-    // ---- the next item's groups are on their way while this one is joined ----
-    pos += run.b - run.a;
-    const bool more = pos < end;
-    if (more) {
-      locate(next);
-      if (!dead)
-        for (int i = 0; i < S; ++i)
-          if (next.lo + i * TG < next.hi) fill(next, next.lo + i * TG);
-    }
-
-    // ---- join the warps ----
+    // ---- the item's end for this warp ----
+    const bool whole = use.a == 0 && use.b == use.n;
     const float down = __uint_as_float(static_cast<uint32_t>(127 - up_exp) << 23);
-    const bool whole = run.a == 0 && run.b == run.n;
-    float *slot = slots + (2 * blockIdx.x + (run.a == 0 ? 1 : 0)) * kv_attn_slot_floats(C::kRows, D);
+    float *slot = warp_slots + (2 * warp + (use.a == 0 ? 1 : 0)) * kSlot;
+    if (!whole && lane == 0) pieces[2 * warp + (use.a == 0 ? 1 : 0)] = Piece{use.seq, use.head, use.tile, use.a, use.b, use.n};
 #pragma unroll
-    for (int mt = 0; mt < MT; ++mt) {
-      if (mt) __syncthreads();  // the previous tile's join has been read
-      sum[mt] += __shfl_xor_sync(0xffffffffu, sum[mt], 1);
-      sum[mt] += __shfl_xor_sync(0xffffffffu, sum[mt], 2);
-      if (t == 0) w_max[warp][g] = top[mt], w_sum[warp][g] = sum[mt];
+    for (int o = 0; o < OCT; ++o) {
+      float l = sum[o] * 0x1p-13f;
+      l += __shfl_xor_sync(0xffffffffu, l, 1);
+      l += __shfl_xor_sync(0xffffffffu, l, 2);
+      const int row = use.tile * C::kRows + o * 8 + g;
+      if (row >= p.rows) continue;
+      const float by = whole ? (l > 0.0f ? down / l : 0.0f) : down;
+      const int64_t out = kv_out_at(p, use.seq, use.head, row, D);
+      float *part = slot + (o * 8 + g) * D;
+      if (!whole && t == 0) *reinterpret_cast<float2 *>(slot + C::kRows * D + (o * 8 + g) * 2) = make_float2(top[o], l);
 #pragma unroll
-      for (int b = 0; b < NB; ++b) {
-        float(*c)[2] = &acc[mt][b * 4];
-        float *row = join + g * C::kRowPad + b * 32 + 4 * t;
-        *reinterpret_cast<float4 *>(row) = make_float4(c[0][0] * down, c[2][0] * down, c[0][1] * down, c[2][1] * down);
-        *reinterpret_cast<float4 *>(row + 16) = make_float4(c[1][0] * down, c[3][0] * down, c[1][1] * down, c[3][1] * down);
+      for (int b = 0; b < NB; ++b)
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {
+          const float2 x = acc[o][b * 4 + half], y = acc[o][b * 4 + half + 2];
+          const float4 v = make_float4(x.x * by, y.x * by, x.y * by, y.y * by);
+          const int d = b * 32 + half * 16 + 4 * t;
+          if (whole)
+            kv_store(p, out + d, v);
+          else
+            *reinterpret_cast<float4 *>(part + d) = v;
+        }
+    }
+    next(use);
+  }
+
+  // ---- the block's partial results, in the line's order ----
+  __syncthreads();
+  for (int e = 0; e < 2 * NW;) {
+    const Piece first = pieces[e];
+    if (first.seq < 0) {
+      ++e;
+      continue;
+    }
+    int stop = e + 1, b = first.b;
+    while (stop < 2 * NW && (pieces[stop].seq < 0 || (pieces[stop].seq == first.seq && pieces[stop].head == first.head &&
+                                                      pieces[stop].tile == first.tile))) {
+      if (pieces[stop].seq >= 0) b = pieces[stop].b;
+      ++stop;
+    }
+    const bool whole = first.a == 0 && b == first.n;
+    float *slot = block_slots + (first.a == 0 ? kSlot : 0);
+    for (int i = tid; i < C::kRows * (D / 4); i += kThreads) {
+      const int r = i / (D / 4), d = (i - r * (D / 4)) * 4, row = first.tile * C::kRows + r;
+      if (row >= p.rows) continue;
+      KvSum x;
+      for (int k = e; k < stop; ++k) {
+        if (pieces[k].seq < 0) continue;
+        const float *s = warp_slots + k * kSlot;
+        const float2 ml = *reinterpret_cast<const float2 *>(s + C::kRows * D + r * 2);
+        x.add(ml.x, ml.y, *reinterpret_cast<const float4 *>(s + r * D + d));
       }
-      __syncthreads();
-      for (int e = tid; e < 8 * (D / 4); e += NW * 32) {
-        const int r = e / (D / 4), d = (e - r * (D / 4)) * 4;
-        const int row = run.tile * C::kRows + mt * 8 + r;
-        if (row >= p.rows) continue;
-        float m = -INFINITY;
-#pragma unroll
-        for (int w = 0; w < NW; ++w) m = fmaxf(m, w_max[w][r]);
-        const float ref = m == -INFINITY ? 0.0f : m;
-        float l = 0.0f;
-        float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-        for (int w = 0; w < NW; ++w) {
-          const float k = exp2_approx(w_max[w][r] - ref);
-          l = fmaf(k, w_sum[w][r], l);
-          const float4 v = *reinterpret_cast<const float4 *>(joins + (w * 8 + r) * C::kRowPad + d);
-          o.x = fmaf(k, v.x, o.x), o.y = fmaf(k, v.y, o.y), o.z = fmaf(k, v.z, o.z), o.w = fmaf(k, v.w, o.w);
-        }
-        if (whole) {
-          const float inv = l > 0.0f ? 1.0f / l : 0.0f;
-          kv_store(p, kv_out_at(p, run.seq, run.head, row, D) + d,
-                   make_float4(o.x * inv, o.y * inv, o.z * inv, o.w * inv));
-        } else {
-          *reinterpret_cast<float4 *>(slot + (mt * 8 + r) * D + d) = o;
-          if (d == 0) *reinterpret_cast<float2 *>(slot + C::kRows * D + (mt * 8 + r) * 2) = make_float2(m, l);
-        }
+      if (whole) {
+        kv_store(p, kv_out_at(p, first.seq, first.head, row, D) + d, x.result());
+      } else {
+        *reinterpret_cast<float4 *>(slot + r * D + d) = x.o;
+        if (d == 0) *reinterpret_cast<float2 *>(slot + C::kRows * D + r * 2) = make_float2(x.m, x.l);
       }
     }
-    if (!more) {
-      // What is left to join: an item that begins here and ends in a later block.
-      if (tid == 0) {
-        KvSplit sp{-1, 0, 0, 0};
-        if (run.a == 0 && run.b < run.n) {
-          const int64_t tail = end - (run.b - run.a) + run.n - 1;  // the item's last group on the line
-          sp = KvSplit{run.seq, run.head, run.tile, static_cast<int>(((tail + 1) * blocks - 1) / total)};
-        }
-        splits[blockIdx.x] = sp;
-      }
-      break;
+    if (!whole && first.a == 0 && tid == 0) {
+      // The item's last unit on the line, and the block that holds it.
+      int64_t at = scan[first.seq / chunk];
+      for (int s = first.seq / chunk * chunk; s < first.seq; ++s) at += kv_units(kv_seq(p, s, status).n) * per_seq;
+      at += (static_cast<int64_t>(first.head) * p.tiles + first.tile + 1) * kv_units(first.n) - 1;
+      splits[blockIdx.x] = KvSplit{first.seq, first.head, first.tile, static_cast<int>(((at + 1) * blocks - 1) / total)};
     }
-    __syncthreads();  // the join and the fragments have been read
-    run = next;
-    load_q(run);
-    __syncthreads();
+    e = stop;
   }
 }
 
-template <int NB, bool KQ8, bool VQ8, int MT>
-__global__ void __launch_bounds__(KvCfg<NB, KQ8, VQ8, MT>::kNW * 32, 1)
+template <int NB, bool KQ8, bool VQ8, int OCT, bool FINE>
+__global__ void __launch_bounds__(KvCfg<NB, KQ8, VQ8, OCT, FINE>::kNW * 32, 1)
     kv_attn_kernel(const __grid_constant__ KvLaunch p, uint32_t *status) {
-  kv_attn_body<NB, KQ8, VQ8, MT>(p, status);
+  kv_attn_body<NB, KQ8, VQ8, OCT, FINE>(p, status);
 }
 
 // Launch of one instance; the attribute is set once per device.
-template <int NB, bool KQ8, bool VQ8, int MT>
+template <int NB, bool KQ8, bool VQ8, int OCT, bool FINE>
 cudaError_t kv_attn_launch(const DevInfo &dev, KvLaunch &p, uint32_t *status, cudaLaunchConfig_t cfg) {
-  using C = KvCfg<NB, KQ8, VQ8, MT>;
+  using C = KvCfg<NB, KQ8, VQ8, OCT, FINE>;
+  const auto kernel = kv_attn_kernel<NB, KQ8, VQ8, OCT, FINE>;
   static DeviceFlags ready;
   if (!ready.done(dev.device)) {
-    cudaError_t e = cudaFuncSetAttribute(kv_attn_kernel<NB, KQ8, VQ8, MT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                         C::kSmem);
+    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
     if (e != cudaSuccess) return e;
     ready.set(dev.device);
   }
   cfg.blockDim = dim3(C::kNW * 32);
   cfg.dynamicSmemBytes = C::kSmem;
   p.tiles = (p.rows + C::kRows - 1) / C::kRows;
-  return cudaLaunchKernelEx(&cfg, kv_attn_kernel<NB, KQ8, VQ8, MT>, p, status);
+  return cudaLaunchKernelEx(&cfg, kernel, p, status);
 }
 
-// Row tiles of a block: the fewest that hold the rows, 16 (block, tile) pairs at
-// most (their sums stay in registers).
-template <int NB>
-constexpr int kv_attn_tiles(int rows) {
-  const int most = NB * 4 <= 16 ? 4 : 2;
-  return rows <= 8 ? 1 : rows <= 16 || most == 2 ? 2 : 4;
+// Octets of rows that a warp takes at a time: the fewest that hold the rows, as
+// many at most as leave their sums in registers.
+constexpr int kv_attn_octets(int nb, int rows, bool fine) {
+  return rows <= 8 ? 1 : rows <= 16 || fine || nb > 4 ? 2 : 4;
 }
 
-template <int NB, bool KQ8, bool VQ8>
+template <int NB, bool KQ8, bool VQ8, bool FINE>
 cudaError_t kv_attn_rows(const DevInfo &dev, KvLaunch &p, uint32_t *status, const cudaLaunchConfig_t &cfg) {
-  switch (kv_attn_tiles<NB>(p.rows)) {
-    case 1: return kv_attn_launch<NB, KQ8, VQ8, 1>(dev, p, status, cfg);
-    case 2: return kv_attn_launch<NB, KQ8, VQ8, 2>(dev, p, status, cfg);
+  switch (kv_attn_octets(NB, p.rows, FINE)) {
+    case 1: return kv_attn_launch<NB, KQ8, VQ8, 1, FINE>(dev, p, status, cfg);
+    case 2: return kv_attn_launch<NB, KQ8, VQ8, 2, FINE>(dev, p, status, cfg);
     default:
-      if constexpr (NB <= 4) return kv_attn_launch<NB, KQ8, VQ8, 4>(dev, p, status, cfg);
+      if constexpr (NB <= 4 && !FINE) return kv_attn_launch<NB, KQ8, VQ8, 4, FINE>(dev, p, status, cfg);
       return cudaErrorInvalidValue;
   }
 }
 
+// fp32 queries in two fp16 terms, bf16 ones (whose outputs keep 8 bits) in one.
+template <int NB, bool KQ8, bool VQ8>
+cudaError_t kv_attn_dtype(const DevInfo &dev, KvLaunch &p, uint32_t *status, const cudaLaunchConfig_t &cfg) {
+  return p.bf16 ? kv_attn_rows<NB, KQ8, VQ8, false>(dev, p, status, cfg)
+                : kv_attn_rows<NB, KQ8, VQ8, true>(dev, p, status, cfg);
+}
+
 template <int NB>
 cudaError_t kv_attn_types(const DevInfo &dev, KvLaunch &p, uint32_t *status, const cudaLaunchConfig_t &cfg) {
-  if (p.f.kq8) return p.f.vq8 ? kv_attn_rows<NB, true, true>(dev, p, status, cfg) : kv_attn_rows<NB, true, false>(dev, p, status, cfg);
-  return p.f.vq8 ? kv_attn_rows<NB, false, true>(dev, p, status, cfg) : kv_attn_rows<NB, false, false>(dev, p, status, cfg);
+  if (p.f.kq8)
+    return p.f.vq8 ? kv_attn_dtype<NB, true, true>(dev, p, status, cfg) : kv_attn_dtype<NB, true, false>(dev, p, status, cfg);
+  return p.f.vq8 ? kv_attn_dtype<NB, false, true>(dev, p, status, cfg) : kv_attn_dtype<NB, false, false>(dev, p, status, cfg);
 }
 
 // kv_attn_d*.cu

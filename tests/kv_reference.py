@@ -121,11 +121,11 @@ class Cache:
 
 
 def attention(q, k, v, length, scale, window=0):
-    """One sequence. q [M, Hq, d], k, v [length, Hkv, d], all float64 -> (out, A, S, F): the result, sum p|v| / sum p
-    per output, per row the largest sum |scale q_d k_jd| over its keys, and the keys times the largest |v|."""
+    """One sequence. q [M, Hq, d], k, v [length, Hkv, d], all float64 -> (out, A, S, floor): the result, sum p|v| / sum p
+    per output, per row the largest sum |scale q_d k_jd| over its keys, and the weights' floor (assert_attention)."""
     m, hq, d = q.shape
     out, a, s = np.zeros(q.shape), np.zeros(q.shape), np.zeros((m, hq, 1))
-    floor = len(v) * np.abs(v).max(initial=0.0)
+    floor = np.abs(v).max(initial=0.0) * min(len(v) * 2.0 ** -28, np.sqrt(len(v)) * 2.0 ** -25)
     ratio = hq // (k.shape[1] if k.ndim == 3 else 1)
     for i in range(m):
         last = length - m + i
@@ -151,25 +151,29 @@ def assert_attention(got, ref, what="", bf16=False):
     turns its weight by the factor exp(e); after the division an output is off by
     at most 2 e A, A = sum p|v| / sum p. The exponentials, the sums over the keys,
     the division and the two-term products (22 bits: 2^-23 each) add at most
-    16 u sqrt(1 + D) A to that in the same sense. bf16 outputs are rounded once
-    more: 2^-8 of the value. Over a whole output the errors do not line up: its
-    2-norm is held to 1e-5 of A's, the library's fp32 tolerance.
+    16 u sqrt(1 + D) A to that in the same sense. Over a whole output the errors
+    do not line up: its 2-norm is held to 1e-5 of A's, the library's fp32
+    tolerance. With bf16 queries the weights p and their products p d_v are rounded
+    to fp16, 2^-11 of each and so 2^-10 A, and the outputs to bf16, 2^-8 of the
+    value.
 
-    The weights p d_v are held as two fp16 terms, at a power of two that brings
-    the largest scale d_v of the keys to 2^14 or more. fp16's smallest step is
-    2^-24, so a weight is off by 2^-25 at least there, that is 2^-39 of the
-    largest d_v, and its product with a code c by 2^-39 |c| max d_v <= 2^-39 *
-    128/127 max|v| (the largest |c| is 8 or 127 and belongs to the largest |v| of
-    its block). Each of the keys may add one such error to an output, and sum p
-    >= 1 divides them: F 2^-38 with F = keys * max|v| covers it. It counts where
-    everything that a dim sees weighs less than about 2^-39.
+    The weights p d_v 2^13 are held as fp16 terms. fp16's smallest step is 2^-24,
+    and the terms lose at most half of one where p is split and twice half of one
+    where the product is: less than 2^-23 (d_v < 2). The largest d_v of the keys
+    taken together is 2^-7 at least, by a power of two where need be, so that
+    is 2^-23 / 2^(13 - 7) = 2^-29 of the largest d_v at most, and with a code c
+    2^-29 |c| max d_v <= 2^-29 128/127 max|v| (the largest |c| is 8 or 127 and
+    belongs to the largest |v| of its block). Each of the keys may add one such
+    error to an output, and sum p >= 1 divides them: F 2^-28 with F = keys *
+    max|v| is the bound. It lines up nowhere: as above, 8 sqrt(keys) of them are
+    taken, F / sqrt(keys) 2^-25, where that is less.
     """
     out, a, s, floor = ref
     got = np.asarray(got, dtype=np.float64)
     assert got.shape == out.shape, (what, got.shape, out.shape)
     assert np.isfinite(got).all(), f"{what}: non-finite outputs"
     u, d = 2.0 ** -24, got.shape[-1]
-    bound = (16 * u * np.sqrt(d) * s + 16 * u * np.sqrt(1 + d)) * a + 2.0 ** -38 * floor + (2.0 ** -8 * np.abs(out) if bf16 else 0)
+    bound = (16 * u * np.sqrt(d) * s + 16 * u * np.sqrt(1 + d)) * a + floor + (2.0 ** -10 * a + 2.0 ** -8 * np.abs(out) if bf16 else 0)
     err = np.abs(got - out)
     bad = err > bound
     if bad.any():
