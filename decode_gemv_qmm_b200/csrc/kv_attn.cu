@@ -61,6 +61,7 @@ qmm_status launch_kv_attn(const DevInfo &dev, const KvForm &f, int dtype, const 
   p.rows = a.m * p.ratio;
   p.min_units = kKvItemCost + 2;
   p.bf16 = dtype == QMM_BF16;
+  p.magic = KvMagic{0x64006400u, 0x2c002c00u, 0xd480d480u};
   void *status = nullptr;
   cudaError_t e = cudaGetSymbolAddress(&status, g_attn_status);
   if (e != cudaSuccess) return cuda_check(e, "kv_attn status");

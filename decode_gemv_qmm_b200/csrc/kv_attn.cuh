@@ -38,18 +38,24 @@ __device__ __forceinline__ void split_f16(float2 x, __half2 &hi, __half2 &lo) {
   lo = __float22half2_rn(__ffma2_rn(__half22float2(hi), make_float2(-1.0f, -1.0f), x));
 }
 
-// Codes as fp16 pairs, exact: 0x6400 | c is 1024 + c.
+// Codes as fp16 pairs, exact: 0x6400 | c is 1024 + c. The constants come as
+// launch arguments: an instruction takes one immediate, and constants that the
+// compiler sees cost a second operation (measured: 64 of 487 instructions of 16
+// keys).
+struct KvMagic {
+  uint32_t k1024, sixteenth, minus72;  // fp16 pairs; 0x64 is also the high byte of 1024 + c
+};
 //   Q4_0: low nibbles of bytes 0 and 2 of w; high nibbles of bytes 0 and 2
-__device__ __forceinline__ uint32_t q4_low(uint32_t w) {
-  return h2_bits(__hsub2(bits_h2((w & 0x000f000fu) | 0x64006400u), bits_h2(0x64086408u)));  // - 1032
+__device__ __forceinline__ uint32_t q4_low(uint32_t w, const KvMagic &k) {
+  return h2_bits(__hsub2(bits_h2((w & 0x000f000fu) | k.k1024), bits_h2(0x64086408u)));  // - 1032
 }
-__device__ __forceinline__ uint32_t q4_high(uint32_t w) {
-  return h2_bits(__hfma2(bits_h2((w & 0x00f000f0u) | 0x64006400u), bits_h2(0x2c002c00u), bits_h2(0xd480d480u)));  // / 16 - 72
+__device__ __forceinline__ uint32_t q4_high(uint32_t w, const KvMagic &k) {
+  return h2_bits(__hfma2(bits_h2((w & 0x00f000f0u) | k.k1024), bits_h2(k.sixteenth), bits_h2(k.minus72)));
 }
 //   Q8_0: two bytes of w (already xor 0x80808080: code + 128) chosen by kSel
 template <uint32_t kSel>
-__device__ __forceinline__ uint32_t q8_pair(uint32_t w) {
-  return h2_bits(__hsub2(bits_h2(__byte_perm(w, 0x64646464u, kSel)), bits_h2(0x64806480u)));  // - 1152
+__device__ __forceinline__ uint32_t q8_pair(uint32_t w, const KvMagic &k) {
+  return h2_bits(__hsub2(bits_h2(__byte_perm(w, k.k1024, kSel)), bits_h2(0x64806480u)));  // - 1152
 }
 
 __device__ __forceinline__ uint2 lds_u2(uint32_t addr) {
@@ -117,6 +123,7 @@ struct KvLaunch {
   int ratio, rows, tiles;  // query heads of a key/value head; rows M ratio of one; tiles of kRows rows
   int min_units;           // least units of the line for a warp
   int bf16;
+  KvMagic magic;
 };
 
 // Groups of 16 tokens that the queries of sequence s see: [first, first + n).
@@ -210,6 +217,7 @@ __device__ __forceinline__ void kv_attn_body(const KvLaunch &p, uint32_t *status
   __shared__ Piece pieces[2 * NW];
 
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, t = lane & 3;
+  const KvMagic magic = p.magic;
   uint8_t *own = smem + warp * C::warp_bytes(TG, S);
   uint4 *qfrag = reinterpret_cast<uint4 *>(own);  // [MT][NB][2][32]
   uint8_t *ring = own + C::kQBytes;
@@ -337,41 +345,54 @@ __device__ __forceinline__ void kv_attn_body(const KvLaunch &p, uint32_t *status
   const int per_page = p.f.page / kKvGroup, page_shift = 31 - __clz(per_page);
   const uint64_t policy = l2_evict_first_policy();
   Place put = use;
-  int put_grp = put.first + put.a;
   uint32_t filled = 0, used = 0;  // stages of the ring so far
   uint32_t ok_bits = 0;           // groups in the ring whose page exists
   bool dead = false;              // a wait ran out
 
-  // Fill the ring's next stage with the next step of TG groups, one lane a group.
-  auto fill = [&]() {
-    if (put.a == put.b) return;
-    const int st = filled % S;
+  // The copies run ahead of the work, over the ends of items. Each lane has the
+  // address of one of the next 32 groups of the item at hand (put_at counts
+  // those copied, put_n those there are, put_ok marks the ones whose page exists).
+  const uint8_t *src = nullptr;
+  int put_at = 0, put_n = 0, put_grp = put.first + put.a;
+  uint32_t put_ok = 0;
+  auto window = [&]() {
     const int grp = put_grp + lane, end = put.first + put.b;
-    int page = -1;
-    if (lane < TG && grp < end) {
-      page = __ldg(p.a.table + put.seq * p.a.table_stride + (grp >> page_shift));
-      if (page < 0 || page >= p.f.pages) {
-        page = -1;
-        atomicOr(status, kDevBadIndex);
-      }
+    put_n = min(end - put_grp, 32);
+    put_at = 0;
+    bool ok = false;
+    if (lane < put_n) {
+      const int page = __ldg(p.a.table + put.seq * p.a.table_stride + (grp >> page_shift));
+      ok = page >= 0 && page < p.f.pages;
+      if (!ok) atomicOr(status, kDevBadIndex);
+      src = p.a.cache + ((static_cast<int64_t>(page) * p.f.heads + put.head) * per_page + (grp & (per_page - 1))) *
+                            C::kGroupBytes;
     }
-    const uint32_t ok = __ballot_sync(0xffffffffu, page >= 0);
-    if (lane == 0) mbar_arrive_expect_tx(bar + st, __popc(ok) * C::kGroupBytes);
+    put_ok = __ballot_sync(0xffffffffu, ok);
+  };
+  // Fill the ring's next stage with the next step of TG groups.
+  auto fill = [&]() {
+    if (put_n == 0) return;
+    const int st = filled % S;
+    const uint32_t ok = put_ok >> put_at & ((1u << TG) - 1);
+    const int mine = lane - put_at;
+    if (mine == 0) mbar_arrive_expect_tx(bar + st, __popc(ok) * C::kGroupBytes);
     __syncwarp();
-    if (page >= 0)
-      bulk_g2s(ring + st * C::kStageBytes + lane * C::kGroupBytes,
-               p.a.cache + ((static_cast<int64_t>(page) * p.f.heads + put.head) * per_page + (grp & (per_page - 1))) *
-                               C::kGroupBytes,
-               C::kGroupBytes, bar + st, policy);
+    if (mine >= 0 && mine < TG && (put_ok >> lane & 1))
+      bulk_g2s(ring + st * C::kStageBytes + mine * C::kGroupBytes, src, C::kGroupBytes, bar + st, policy);
     ok_bits = (ok_bits & ~(((1u << TG) - 1) << (st * TG))) | ok << (st * TG);
     ++filled;
-    put_grp += TG;
-    if (put_grp >= end) {
-      next(put);
-      put_grp = put.first + put.a;
+    put_at += TG;
+    if (put_at >= put_n) {
+      put_grp += put_n;
+      if (put_grp >= put.first + put.b) {
+        next(put);
+        put_grp = put.first + put.a;
+      }
+      window();
     }
   };
 
+  window();
   for (int i = 0; i < S; ++i) fill();
 
   while (use.a < use.b && !dead) {
@@ -469,6 +490,68 @@ __device__ __forceinline__ void kv_attn_body(const KvLaunch &p, uint32_t *status
       const bool full = ok == (1u << TG) - 1 && key0 + TG * kKvGroup <= use.len - p.a.m + 1 &&
                         (p.a.window == 0 || key0 >= use.len - p.a.window);
 
+      // ---- scales of the values ----
+      uint32_t vs[TG][NB][2];
+#pragma unroll
+      for (int gi = 0; gi < TG; ++gi) {
+        const uint32_t at = stage + gi * C::kGroupBytes + C::kKeyPart + kv_code_bytes(NB, VQ8) + t * NB * 8;
+#pragma unroll
+        for (int b = 0; b < NB; b += 2) {
+          if (NB % 2 == 0) {
+            const uint4 v = lds_u4(at + b * 8);
+            vs[gi][b][0] = v.x, vs[gi][b][1] = v.y, vs[gi][min(b + 1, NB - 1)][0] = v.z, vs[gi][min(b + 1, NB - 1)][1] = v.w;
+          } else {
+            const uint2 v = lds_u2(at + b * 8);
+            vs[gi][b][0] = v.x, vs[gi][b][1] = v.y;
+            if (b + 1 < NB) {
+              const uint2 u = lds_u2(at + b * 8 + 8);
+              vs[gi][min(b + 1, NB - 1)][0] = u.x, vs[gi][min(b + 1, NB - 1)][1] = u.y;
+            }
+          }
+        }
+      }
+      if (!full) {  // what no row sees may be anything, NaN among it: its scale is 0
+#pragma unroll
+        for (int gi = 0; gi < TG; ++gi)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {  // e = tok / 4: column e & 1 of half e >> 1
+            const int key = key0 + gi * kKvGroup + t + 4 * e;
+            if (!(ok >> gi & 1) || key >= use.len || key < low_all)
+#pragma unroll
+              for (int b = 0; b < NB; ++b) vs[gi][b][e >> 1] &= e & 1 ? 0x0000ffffu : 0xffff0000u;
+          }
+      }
+      // The weights are p 2^13 and so p d_v 2^13: inside fp16 with room for both
+      // terms while the largest scale is in [2^-7, 2). Outside, the scales of the
+      // step are brought there by a power of two, which the sums keep (up_exp).
+      uint32_t bits = 0;
+#pragma unroll
+      for (int gi = 0; gi < TG; ++gi)
+#pragma unroll
+        for (int b = 0; b < NB; ++b) bits |= vs[gi][b][0] | vs[gi][b][1];
+      bits = __reduce_or_sync(0xffffffffu, bits & 0x60006000u);
+      int e_new = 13;
+      if (((bits | bits >> 16) & 0x6000u) != 0x2000u) {
+        uint32_t big = 0;
+#pragma unroll
+        for (int gi = 0; gi < TG; ++gi)
+#pragma unroll
+          for (int b = 0; b < NB; ++b)
+            big = __vmaxu2(big, __vmaxu2(vs[gi][b][0] & 0x7fff7fffu, vs[gi][b][1] & 0x7fff7fffu));
+        big = __reduce_max_sync(0xffffffffu, max(big & 0xffffu, big >> 16));
+        const int by = 14 - static_cast<int>(max(big >> 10, 1u));  // -17 .. 13: two factors of fp16
+        e_new += by;
+        const int by1 = by / 2, by2 = by - by1;
+        const uint32_t f1 = static_cast<uint32_t>(by1 + 15) << 10, f2 = static_cast<uint32_t>(by2 + 15) << 10;
+#pragma unroll
+        for (int gi = 0; gi < TG; ++gi)
+#pragma unroll
+          for (int b = 0; b < NB; ++b)
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+              vs[gi][b][h] = h2_bits(__hmul2(__hmul2(bits_h2(vs[gi][b][h]), bits_h2(f1 | f1 << 16)), bits_h2(f2 | f2 << 16)));
+      }
+
       // ---- scores ----
       float2 z[OCT][TG][2];
 #pragma unroll
@@ -511,11 +594,11 @@ __device__ __forceinline__ void kv_attn_body(const KvLaunch &p, uint32_t *status
               uint32_t k00, k01, k10, k11;
               if (KQ8) {
                 const uint32_t w0 = kw[gi][j][(2 * r) & 3] ^ 0x80808080u, w1 = kw[gi][j][(2 * r + 1) & 3] ^ 0x80808080u;
-                k00 = q8_pair<0x4240>(w0), k01 = q8_pair<0x4341>(w0);
-                k10 = q8_pair<0x4240>(w1), k11 = q8_pair<0x4341>(w1);
+                k00 = q8_pair<0x5250>(w0, magic), k01 = q8_pair<0x5351>(w0, magic);
+                k10 = q8_pair<0x5250>(w1, magic), k11 = q8_pair<0x5351>(w1, magic);
               } else {
                 const uint32_t w = kw[gi][j][r], w8 = w >> 8;
-                k00 = q4_low(w), k01 = q4_low(w8), k10 = q4_high(w), k11 = q4_high(w8);
+                k00 = q4_low(w, magic), k01 = q4_low(w8, magic), k10 = q4_high(w, magic), k11 = q4_high(w8, magic);
               }
               const float2 d = __half22float2(bits_h2(j ? ks.y : ks.x));
 #pragma unroll
@@ -536,72 +619,17 @@ __device__ __forceinline__ void kv_attn_body(const KvLaunch &p, uint32_t *status
         first += n;
       }
 
-      // ---- scales of the values, and what the masks leave ----
-      uint32_t vs[TG][NB][2];
-#pragma unroll
-      for (int gi = 0; gi < TG; ++gi) {
-        const uint32_t at = stage + gi * C::kGroupBytes + C::kKeyPart + kv_code_bytes(NB, VQ8) + t * NB * 8;
-#pragma unroll
-        for (int b = 0; b < NB; b += 2) {
-          if (NB % 2 == 0) {
-            const uint4 v = lds_u4(at + b * 8);
-            vs[gi][b][0] = v.x, vs[gi][b][1] = v.y, vs[gi][min(b + 1, NB - 1)][0] = v.z, vs[gi][min(b + 1, NB - 1)][1] = v.w;
-          } else {
-            const uint2 v = lds_u2(at + b * 8);
-            vs[gi][b][0] = v.x, vs[gi][b][1] = v.y;
-            if (b + 1 < NB) {
-              const uint2 u = lds_u2(at + b * 8 + 8);
-              vs[gi][min(b + 1, NB - 1)][0] = u.x, vs[gi][min(b + 1, NB - 1)][1] = u.y;
-            }
-          }
-        }
-      }
       if (!full) {
 #pragma unroll
-        for (int gi = 0; gi < TG; ++gi) {
-          const bool there = ok >> gi & 1;
+        for (int gi = 0; gi < TG; ++gi)
 #pragma unroll
-          for (int e = 0; e < 4; ++e) {  // e = tok / 4: column e & 1 of half e >> 1
+          for (int e = 0; e < 4; ++e) {
             const int key = key0 + gi * kKvGroup + t + 4 * e;
 #pragma unroll
             for (int o = 0; o < OCT; ++o)
-              if (!there || key > last[o] || key < low[o]) (e & 1 ? z[o][gi][e >> 1].y : z[o][gi][e >> 1].x) = -INFINITY;
-            // what no row sees may be anything, NaN among it: its scale is 0
-            if (!there || key >= use.len || key < low_all)
-#pragma unroll
-              for (int b = 0; b < NB; ++b) vs[gi][b][e >> 1] &= e & 1 ? 0x0000ffffu : 0xffff0000u;
+              if (!(ok >> gi & 1) || key > last[o] || key < low[o])
+                (e & 1 ? z[o][gi][e >> 1].y : z[o][gi][e >> 1].x) = -INFINITY;
           }
-        }
-      }
-      // The weights are p 2^13 and so p d_v 2^13: inside fp16 with room for both
-      // terms while the largest scale is in [2^-7, 2). Outside, the scales of the
-      // step are brought there by a power of two, which the sums keep (up_exp).
-      uint32_t bits = 0;
-#pragma unroll
-      for (int gi = 0; gi < TG; ++gi)
-#pragma unroll
-        for (int b = 0; b < NB; ++b) bits |= vs[gi][b][0] | vs[gi][b][1];
-      bits = __reduce_or_sync(0xffffffffu, bits & 0x60006000u);
-      int e_new = 13;
-      if (((bits | bits >> 16) & 0x6000u) != 0x2000u) {
-        uint32_t big = 0;
-#pragma unroll
-        for (int gi = 0; gi < TG; ++gi)
-#pragma unroll
-          for (int b = 0; b < NB; ++b)
-            big = __vmaxu2(big, __vmaxu2(vs[gi][b][0] & 0x7fff7fffu, vs[gi][b][1] & 0x7fff7fffu));
-        big = __reduce_max_sync(0xffffffffu, max(big & 0xffffu, big >> 16));
-        const int by = 14 - static_cast<int>(max(big >> 10, 1u));  // -17 .. 13: two factors of fp16
-        e_new += by;
-        const int by1 = by / 2, by2 = by - by1;
-        const uint32_t f1 = static_cast<uint32_t>(by1 + 15) << 10, f2 = static_cast<uint32_t>(by2 + 15) << 10;
-#pragma unroll
-        for (int gi = 0; gi < TG; ++gi)
-#pragma unroll
-          for (int b = 0; b < NB; ++b)
-#pragma unroll
-            for (int h = 0; h < 2; ++h)
-              vs[gi][b][h] = h2_bits(__hmul2(__hmul2(bits_h2(vs[gi][b][h]), bits_h2(f1 | f1 << 16)), bits_h2(f2 | f2 << 16)));
       }
 
       // ---- running maximum and sum ----
@@ -669,13 +697,13 @@ __device__ __forceinline__ void kv_attn_body(const KvLaunch &p, uint32_t *status
               if (VQ8) {
                 const uint32_t w0 = vw[gi][2 * h][r & 1] ^ 0x80808080u, w1 = vw[gi][2 * h + 1][r & 1] ^ 0x80808080u;
                 const uint32_t x = __byte_perm(w0, w1, 0x5140), y = __byte_perm(w0, w1, 0x7362);
-                vb[gi][0][h] = q8_pair<0x4140>(x), vb[gi][2][h] = q8_pair<0x4342>(x);
-                vb[gi][1][h] = q8_pair<0x4140>(y), vb[gi][3][h] = q8_pair<0x4342>(y);
+                vb[gi][0][h] = q8_pair<0x5150>(x, magic), vb[gi][2][h] = q8_pair<0x5352>(x, magic);
+                vb[gi][1][h] = q8_pair<0x5150>(y, magic), vb[gi][3][h] = q8_pair<0x5352>(y, magic);
               } else {
                 const uint32_t x = __byte_perm(vw[gi][2 * h][r >> 1], vw[gi][2 * h + 1][r >> 1], r & 1 ? 0x7632 : 0x5410);
                 const uint32_t x8 = x >> 8;
-                vb[gi][0][h] = q4_low(x), vb[gi][1][h] = q4_high(x);
-                vb[gi][2][h] = q4_low(x8), vb[gi][3][h] = q4_high(x8);
+                vb[gi][0][h] = q4_low(x, magic), vb[gi][1][h] = q4_high(x, magic);
+                vb[gi][2][h] = q4_low(x8, magic), vb[gi][3][h] = q4_high(x8, magic);
               }
             }
 #pragma unroll
