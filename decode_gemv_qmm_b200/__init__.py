@@ -10,6 +10,7 @@ there is no fallback of any kind.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 
 import torch
@@ -318,93 +319,104 @@ def qmm_prefill_plan(wtype: int, M: int, N: int, K: int, *, block: int = BLOCK) 
 
 
 # ---- quantised key/value cache ---------------------------------------------
+#
+# These calls are short on the GPU, so the checks here are plain comparisons and
+# messages are only made for what is refused.
 
 _KV_DTYPES = {torch.float32: QMM_F32, torch.bfloat16: QMM_BF16}
 
 
-def _need(ok: bool, fn: str, what: str):
-    if not ok:
-        raise ValueError(f"{fn}: {what}")
+def _kv_refuse(fn: str, what: str):
+    raise ValueError(f"{fn}: {what}")
 
 
-def _kv_cache(fn: str, cache: torch.Tensor, Hkv: int, D: int, page: int, ktype: int, vtype: int, block: int) -> int:
+def _kv_cache(fn: str, cache: torch.Tensor, size: int) -> int:
     """Pages of a cache tensor (uint8 [pages, page_bytes], contiguous), checked against its form."""
-    _need(cache.dtype == torch.uint8 and cache.dim() == 2 and cache.is_contiguous(), fn,
-          "cache is not a contiguous uint8 tensor [pages, page_bytes]")
-    size = qmm_kv_page_bytes(Hkv, D, page=page, ktype=ktype, vtype=vtype, block=block)
-    _need(cache.shape[1] == size, fn, f"pages of {cache.shape[1]} bytes, this form has {size}")
-    return cache.shape[0]
+    if cache.dtype is not torch.uint8 or cache.dim() != 2 or not cache.is_contiguous():
+        _kv_refuse(fn, "cache is not a contiguous uint8 tensor [pages, page_bytes]")
+    pages, held = cache.shape
+    if held != size:
+        _kv_refuse(fn, f"pages of {held} bytes, this form has {size}")
+    return pages
 
 
-def _kv_rows(fn: str, name: str, t: torch.Tensor, dims: int, like: torch.Tensor):
-    _need(t.dim() == dims and (t.stride(-1) == 1 or t.shape[-1] == 1 or t.numel() == 0), fn,
-          f"{name} is not a tensor of {dims} dims with contiguous rows")
-    _need(t.dtype in _KV_DTYPES, fn, f"{name} is {t.dtype}, not float32 or bfloat16")
-    _need(t.device == like.device, fn, f"{name} is on {t.device}, the cache on {like.device}")
+def _kv_rows(fn: str, name: str, t: torch.Tensor, dims: int, dev):
+    """(element type, shape, strides of the leading dims) of a tensor of rows; the stride of a dim that is not stepped
+    over is arbitrary and taken as 0."""
+    dtype, shape, stride = _KV_DTYPES.get(t.dtype), t.shape, t.stride()
+    if dtype is None:
+        _kv_refuse(fn, f"{name} is {t.dtype}, not float32 or bfloat16")
+    if len(shape) != dims or (stride[-1] != 1 and shape[-1] != 1 and t.numel()):
+        _kv_refuse(fn, f"{name} is not a tensor of {dims} dims with contiguous rows")
+    if t.device != dev:
+        _kv_refuse(fn, f"{name} is on {t.device}, the cache on {dev}")
+    if 1 in shape or 0 in shape:
+        none = 0 in shape
+        stride = [0 if n == 1 or none else v for n, v in zip(shape, stride)]
+    return dtype, shape, stride
 
 
-def _strides(t: torch.Tensor, dims: int):
-    """Strides of the leading dims; 0 where a dim is not stepped over (its stride is arbitrary)."""
-    return [t.stride(i) if t.shape[i] > 1 and t.numel() else 0 for i in range(dims)]
+def _kv_index(fn: str, name: str, t: torch.Tensor, dtype, n: int, dev):
+    if t.dtype is not dtype or t.device != dev or t.shape != (n,) or not t.is_contiguous():
+        _kv_refuse(fn, f"{name} is not a contiguous {dtype} tensor of {n} on {dev}")
 
 
-def _kv_index(fn: str, name: str, t: torch.Tensor, dtype, like: torch.Tensor):
-    _need(t.dtype == dtype and t.device == like.device, fn, f"{name} is not a {dtype} tensor on {like.device}")
+_raw_stream = torch._C._cuda_getCurrentRawStream  # the current stream of a device, as an integer
 
 
-class _KvCall:
-    """Device and stream of a call: the tensors' device is made the current one, and what the call
-    allocates belongs to the stream that it runs on."""
+def _kv_elsewhere(dev: torch.device, stream) -> bool:
+    """Whether a call has to switch its device or stream first."""
+    return dev.type == "cuda" and (stream is not None or dev.index != torch.cuda.current_device())
 
-    def __init__(self, like: torch.Tensor, stream):
-        self.dev = like.device
-        if self.dev.type != "cuda":
-            self.ctx, self.stream = None, 0 if stream is None else _stream(stream)
-            return
-        here = self.dev.index == torch.cuda.current_device()
-        if stream is None:
-            self.ctx = None if here else torch.cuda.device(self.dev)
-            self.stream = torch.cuda.current_stream(self.dev).cuda_stream
-        else:
-            if isinstance(stream, int):
-                stream = torch.cuda.ExternalStream(stream, device=self.dev) if stream else torch.cuda.default_stream(self.dev)
-            _need(stream.device == self.dev, "stream", f"the stream is on {stream.device}, the tensors on {self.dev}")
-            self.ctx, self.stream = torch.cuda.stream(stream), stream.cuda_stream
 
-    def __enter__(self):
-        if self.ctx is not None:
-            self.ctx.__enter__()
-        return self.stream
+def _kv_switch(fn: str, dev: torch.device, stream):
+    """Context in which the tensors' device and the call's stream are the current ones, so that what the call
+    allocates belongs to that stream."""
+    if stream is None:
+        return torch.cuda.device(dev)
+    if isinstance(stream, int):
+        stream = torch.cuda.ExternalStream(stream, device=dev) if stream else torch.cuda.default_stream(dev)
+    if stream.device != dev:
+        _kv_refuse(fn, f"the stream is on {stream.device}, the cache on {dev}")
+    return torch.cuda.stream(stream)
 
-    def __exit__(self, *exc):
-        if self.ctx is not None:
-            self.ctx.__exit__(*exc)
+
+def _kv_current(dev: torch.device) -> int:
+    return _raw_stream(dev.index) if dev.type == "cuda" else 0
+
+
+@functools.lru_cache(maxsize=None)
+def _kv_page_bytes(Hkv, D, page, ktype, vtype, block) -> int:
+    out = ctypes.c_int64(0)
+    _check(lib.qmm_kv_page_bytes(ktype, vtype, Hkv, D, block, page, ctypes.addressof(out)), "qmm_kv_page_bytes")
+    return out.value
 
 
 def qmm_kv_page_bytes(Hkv: int, D: int, *, page: int, ktype: int = QMM_Q4_0, vtype: int = QMM_Q4_0,
                       block: int = BLOCK) -> int:
     """Bytes of a page of a key/value cache of this form."""
-    out = ctypes.c_int64(0)
-    _check(lib.qmm_kv_page_bytes(ktype, vtype, Hkv, D, block, page, ctypes.addressof(out)), "qmm_kv_page_bytes")
-    return out.value
+    return _kv_page_bytes(Hkv, D, page, ktype, vtype, block)
 
 
 def qmm_kv_write(cache: torch.Tensor, K: torch.Tensor, V: torch.Tensor, slots: torch.Tensor, *, page: int,
                  ktype: int = QMM_Q4_0, vtype: int = QMM_Q4_0, block: int = BLOCK, stream=None) -> torch.Tensor:
     """Quantise K, V [T, Hkv, D] (fp32 or bf16, rows contiguous) into the cache's slots int64 [T] (negative: left
     out; the others have to differ). cache: uint8 [pages, qmm_kv_page_bytes(Hkv, D, ...)]."""
-    fn = "qmm_kv_write"
-    _kv_rows(fn, "K", K, 3, cache)
-    _kv_rows(fn, "V", V, 3, cache)
-    T, Hkv, D = K.shape
-    _need(V.shape == K.shape and V.dtype == K.dtype, fn, "V is not of K's shape and type")
-    _kv_index(fn, "slots", slots, torch.int64, cache)
-    _need(slots.shape == (T,) and slots.is_contiguous(), fn, f"slots is not a contiguous tensor of {T}")
-    pages = _kv_cache(fn, cache, Hkv, D, page, ktype, vtype, block)
-    with _KvCall(cache, stream) as s:
-        _check(lib.qmm_kv_write(ktype, vtype, _KV_DTYPES[K.dtype], T, Hkv, D, block, pages, page, K.data_ptr(),
-                                *_strides(K, 2), V.data_ptr(), *_strides(V, 2), slots.data_ptr(), cache.data_ptr(),
-                                s), fn)
+    fn, dev = "qmm_kv_write", cache.device
+    if _kv_elsewhere(dev, stream):
+        with _kv_switch(fn, dev, stream):
+            return qmm_kv_write(cache, K, V, slots, page=page, ktype=ktype, vtype=vtype, block=block)
+    dtype, shape, ks = _kv_rows(fn, "K", K, 3, dev)
+    vtype_, vshape, vs = _kv_rows(fn, "V", V, 3, dev)
+    if vshape != shape or vtype_ != dtype:
+        _kv_refuse(fn, "V is not of K's shape and type")
+    T, Hkv, D = shape
+    _kv_index(fn, "slots", slots, torch.int64, T, dev)
+    pages = _kv_cache(fn, cache, _kv_page_bytes(Hkv, D, page, ktype, vtype, block))
+    st = lib.qmm_kv_write(ktype, vtype, dtype, T, Hkv, D, block, pages, page, K.data_ptr(), ks[0], ks[1], V.data_ptr(),
+                          vs[0], vs[1], slots.data_ptr(), cache.data_ptr(), _kv_current(dev))
+    if st:
+        _check(st, fn)
     return cache
 
 
@@ -413,23 +425,32 @@ def qmm_kv_read(cache: torch.Tensor, slots: torch.Tensor, Hkv: int, D: int, K: t
                 dtype: torch.dtype = torch.float32, block: int = BLOCK, stream=None):
     """(K, V) [T, Hkv, D]: the values of the cached tokens at slots int64 [T] (rows of a negative slot are left as
     they were). dtype: float32 or bfloat16, that of K and V where they are given."""
-    fn = "qmm_kv_read"
-    T = slots.shape[0]
-    _kv_index(fn, "slots", slots, torch.int64, cache)
-    _need(slots.dim() == 1 and slots.is_contiguous(), fn, "slots is not a contiguous tensor of one dim")
-    pages = _kv_cache(fn, cache, Hkv, D, page, ktype, vtype, block)
-    with _KvCall(cache, stream) as s:
-        K = _out(K, (T, Hkv, D), cache.device, dtype)
-        V = _out(V, (T, Hkv, D), cache.device, dtype)
-        for name, t in (("K", K), ("V", V)):
-            _kv_rows(fn, name, t, 3, cache)
-            _need(t.shape == (T, Hkv, D) and t.is_contiguous(), fn, f"{name} is not a contiguous {(T, Hkv, D)}")
-        _need(K.dtype == V.dtype, fn, "K and V differ in type")
-        _check(lib.qmm_kv_read(ktype, vtype, _KV_DTYPES[K.dtype], T, Hkv, D, block, pages, page, slots.data_ptr(),
-                               cache.data_ptr(), K.data_ptr(), V.data_ptr(), s), fn)
+    fn, dev = "qmm_kv_read", cache.device
+    if _kv_elsewhere(dev, stream):
+        with _kv_switch(fn, dev, stream):
+            return qmm_kv_read(cache, slots, Hkv, D, K, V, page=page, ktype=ktype, vtype=vtype, dtype=dtype, block=block)
+    T = slots.numel()
+    _kv_index(fn, "slots", slots, torch.int64, T, dev)
+    pages = _kv_cache(fn, cache, _kv_page_bytes(Hkv, D, page, ktype, vtype, block))
+    shape = (T, Hkv, D)
+    if K is None or V is None:
+        if dtype not in _KV_DTYPES:
+            _kv_refuse(fn, f"dtype is {dtype}, not float32 or bfloat16")
+        K = torch.empty(shape, dtype=dtype, device=dev) if K is None else K
+        V = torch.empty_like(K) if V is None else V
+    for t in (K, V):
+        if t.shape != shape or not t.is_contiguous() or t.device != dev or t.dtype not in _KV_DTYPES:
+            _kv_refuse(fn, f"K or V is not a contiguous fp32 or bf16 tensor {shape} on {dev}")
+    if K.dtype is not V.dtype:
+        _kv_refuse(fn, "K and V differ in type")
+    st = lib.qmm_kv_read(ktype, vtype, _KV_DTYPES[K.dtype], T, Hkv, D, block, pages, page, slots.data_ptr(),
+                         cache.data_ptr(), K.data_ptr(), V.data_ptr(), _kv_current(dev))
+    if st:
+        _check(st, fn)
     return K, V
 
 
+@functools.lru_cache(maxsize=None)
 def qmm_kv_attn_workspace(B: int, M: int, Hq: int, Hkv: int, D: int) -> int:
     """Scratch bytes of qmm_kv_attn for these sizes."""
     out = ctypes.c_int64(0)
@@ -445,26 +466,33 @@ def qmm_kv_attn(Q: torch.Tensor, cache: torch.Tensor, table: torch.Tensor, lens:
     sequence, its last M tokens, over its lens int32 [B] cached tokens; table int32 [B, max_pages] names the pages.
     scale: D ** -0.5 by default; window: how many keys a query sees (0: all up to its own). ws: uint8 scratch of
     qmm_kv_attn_workspace(...) bytes, allocated by default; calls that may run at the same time need their own."""
-    fn = "qmm_kv_attn"
-    _kv_rows(fn, "Q", Q, 4, cache)
-    B, M, Hq, D = Q.shape
-    _kv_index(fn, "table", table, torch.int32, cache)
-    _need(table.dim() == 2 and table.shape[0] == B and (table.shape[1] <= 1 or table.stride(1) == 1), fn,
-          f"table is not a tensor of {B} contiguous rows")
-    _kv_index(fn, "lens", lens, torch.int32, cache)
-    _need(lens.shape == (B,) and lens.is_contiguous(), fn, f"lens is not a contiguous tensor of {B}")
-    pages = _kv_cache(fn, cache, Hkv, D, page, ktype, vtype, block)
+    fn, dev = "qmm_kv_attn", cache.device
+    if _kv_elsewhere(dev, stream):
+        with _kv_switch(fn, dev, stream):
+            return qmm_kv_attn(Q, cache, table, lens, Hkv, Y, ws, page=page, ktype=ktype, vtype=vtype, scale=scale,
+                               window=window, block=block)
+    dtype, shape, qs = _kv_rows(fn, "Q", Q, 4, dev)
+    B, M, Hq, D = shape
+    if table.dtype is not torch.int32 or table.device != dev or table.dim() != 2 or table.shape[0] != B:
+        _kv_refuse(fn, f"table is not an int32 tensor of {B} rows on {dev}")
+    held, ts = table.shape[1], table.stride()
+    if held > 1 and ts[1] != 1:
+        _kv_refuse(fn, "table's rows are not contiguous")
+    _kv_index(fn, "lens", lens, torch.int32, B, dev)
+    pages = _kv_cache(fn, cache, _kv_page_bytes(Hkv, D, page, ktype, vtype, block))
     need = qmm_kv_attn_workspace(B, M, Hq, Hkv, D)
-    with _KvCall(cache, stream) as s:
-        Y = _out(Y, (B, M, Hq, D), cache.device, Q.dtype)
-        _need(Y.shape == Q.shape and Y.dtype == Q.dtype and Y.device == cache.device and Y.is_contiguous(), fn,
-              "Y is not a contiguous tensor of Q's shape, type and device")
-        if ws is None:
-            ws = torch.empty(need, dtype=torch.uint8, device=cache.device)
-        _need(ws.dtype == torch.uint8 and ws.is_contiguous() and ws.device == cache.device, fn,
-              "ws is not a contiguous uint8 tensor on the cache's device")
-        _check(lib.qmm_kv_attn(ktype, vtype, _KV_DTYPES[Q.dtype], B, M, Hq, Hkv, D, block, pages, page, Q.data_ptr(),
-                               *_strides(Q, 3), cache.data_ptr(), table.data_ptr(), *_strides(table, 1),
-                               table.shape[1], lens.data_ptr(), D ** -0.5 if scale is None else scale,
-                               window, Y.data_ptr(), ws.data_ptr(), ws.numel(), s), fn)
+    if Y is None:
+        Y = Q.new_empty(shape)
+    elif Y.shape != shape or Y.dtype is not Q.dtype or Y.device != dev or not Y.is_contiguous():
+        _kv_refuse(fn, "Y is not a contiguous tensor of Q's shape, type and device")
+    if ws is None:
+        ws = cache.new_empty(need)
+    elif ws.dtype is not torch.uint8 or ws.device != dev or not ws.is_contiguous():
+        _kv_refuse(fn, "ws is not a contiguous uint8 tensor on the cache's device")
+    st = lib.qmm_kv_attn(ktype, vtype, dtype, B, M, Hq, Hkv, D, block, pages, page, Q.data_ptr(), qs[0], qs[1], qs[2],
+                         cache.data_ptr(), table.data_ptr(), ts[0] if B > 1 and held else 0, held, lens.data_ptr(),
+                         D ** -0.5 if scale is None else scale, window, Y.data_ptr(), ws.data_ptr(), ws.numel(),
+                         _kv_current(dev))
+    if st:
+        _check(st, fn)
     return Y

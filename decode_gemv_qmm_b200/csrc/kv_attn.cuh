@@ -69,11 +69,6 @@ __device__ __forceinline__ uint2 lds_u2(uint32_t addr) {
 // Floats of one partial result: rows x (D + maximum and sum).
 __host__ __device__ constexpr int64_t kv_attn_slot_floats(int rows, int d) { return static_cast<int64_t>(rows) * (d + 2); }
 
-// An item that begins in a block and ends in a later one: what the second launch joins.
-struct KvSplit {
-  int seq, head, tile, last;  // seq < 0: none; last: the block that holds the item's end
-};
-
 constexpr int kKvMaxBlocks = 160;  // most blocks of a launch
 constexpr int kKvMaxWarps = 8;     // most warps of a block
 #ifndef KV_ITEM_COST
@@ -81,9 +76,9 @@ constexpr int kKvMaxWarps = 8;     // most warps of a block
 #endif
 constexpr int kKvItemCost = KV_ITEM_COST;  // what beginning an item costs, in groups
 
-// Scratch: the blocks' KvSplit, two partial results of each block, two of each warp.
+// Scratch: a counter for each block, two partial results of each block, two of each warp.
 __host__ __device__ constexpr int64_t kv_attn_scratch_floats(int rows, int d) {
-  return kKvMaxBlocks * (4 + 2 * (1 + kKvMaxWarps) * kv_attn_slot_floats(rows, d));
+  return kKvMaxBlocks * (4 + 2 * kv_attn_slot_floats(rows, d) + 2 * kKvMaxWarps * rows * d);
 }
 
 template <int NB, bool KQ8, bool VQ8, int OCT, bool FINE>
@@ -95,15 +90,21 @@ struct KvCfg {
   static constexpr int kMT = FINE ? OCT : (OCT + 1) / 2;  // 16-row tiles: eight rows in two terms, or sixteen
   static constexpr int kQBytes = kMT * NB * 1024;         // a warp's query fragments
   static constexpr int kBudget = 222 * 1024;
-#ifndef KV_TG
-#define KV_TG 2
+#ifndef KV_TG1
+#define KV_TG1 4
+#endif
+#ifndef KV_TG4
+#define KV_TG4 1
 #endif
 #ifndef KV_NW
 #define KV_NW 8
 #endif
   static constexpr int warp_bytes(int tg, int stages) { return kQBytes + stages * tg * kGroupBytes; }
   static constexpr int kNW = KV_NW * warp_bytes(1, 2) <= kBudget ? KV_NW : KV_NW / 2;
-  static constexpr int kTG = kGroupBytes <= 4608 && kNW * warp_bytes(KV_TG, 2) <= kBudget ? KV_TG : 1;  // groups of a step
+  // groups of a step
+  static constexpr int kMaxTG = OCT == 1 ? KV_TG1 : OCT == 2 ? 2 : KV_TG4;
+  static constexpr bool fits(int tg) { return tg * kGroupBytes <= 9216 && kNW * warp_bytes(tg, 2) <= kBudget; }
+  static constexpr int kTG = kMaxTG >= 4 && fits(4) ? 4 : kMaxTG >= 2 && fits(2) ? 2 : 1;
   static constexpr int stages() {
     int n = 2;
     while (n < 4 && kNW * warp_bytes(kTG, n + 1) <= kBudget) ++n;
@@ -113,6 +114,7 @@ struct KvCfg {
   static constexpr int kStageBytes = kTG * kGroupBytes;
   static constexpr int kSmem = kNW * warp_bytes(kTG, kStages);
   static_assert(kSmem <= kBudget, "stages do not fit");
+  static_assert(warp_bytes(kTG, kStages) >= kRows * kD * 4, "a warp's partial result does not fit");
   static_assert(kNW <= kKvMaxWarps, "scratch is sized for fewer warps");
 };
 
@@ -124,6 +126,7 @@ struct KvLaunch {
   int min_units;           // least units of the line for a warp
   int bf16;
   KvMagic magic;
+  uint64_t epoch;          // marks this call's counters
 };
 
 // Groups of 16 tokens that the queries of sequence s see: [first, first + n).
@@ -165,17 +168,39 @@ __device__ __forceinline__ int64_t kv_out_at(const KvLaunch &p, int s, int head,
   return ((static_cast<int64_t>(s) * p.a.m + i) * p.a.hq + head * p.ratio + h) * d;
 }
 
-// Four dims of a row, added up over partial results.
+// a * b / c without the slow 64-bit division where the numbers are small.
+__device__ __forceinline__ int64_t kv_muldiv(int64_t a, int64_t b, int64_t c) {
+  const int64_t x = a * b;
+  if ((static_cast<uint64_t>(x | c) >> 32) == 0) return static_cast<uint32_t>(x) / static_cast<uint32_t>(c);
+  return x / c;
+}
+
+// The block that has place `at` of the line, block i's run being [i total / blocks,
+// (i + 1) total / blocks).
+__device__ __forceinline__ int kv_block_of(int64_t at, int64_t blocks, int64_t total) {
+  const int64_t x = (at + 1) * blocks - 1;
+  return static_cast<int>(kv_muldiv(x, 1, total));
+}
+
+// Four dims of a row, added up over partial results (maximum, sum; outputs), a
+// batch of them at a time so that their loads are in flight together.
 struct KvSum {
   float m = -INFINITY, l = 0.0f;
   float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-  __device__ __forceinline__ void add(float m2, float l2, float4 v) {
-    const float next = fmaxf(m, m2), ref = next == -INFINITY ? 0.0f : next;
-    const float keep = exp2_approx(m - ref), k = exp2_approx(m2 - ref);
+  template <int N>
+  __device__ __forceinline__ void add(const float2 (&ml)[N], const float4 (&v)[N]) {
+    float next = m;
+#pragma unroll
+    for (int i = 0; i < N; ++i) next = fmaxf(next, ml[i].x);
+    const float ref = next == -INFINITY ? 0.0f : next, keep = exp2_approx(m - ref);
     m = next;
-    l = fmaf(l, keep, k * l2);
-    o.x = fmaf(o.x, keep, k * v.x), o.y = fmaf(o.y, keep, k * v.y);
-    o.z = fmaf(o.z, keep, k * v.z), o.w = fmaf(o.w, keep, k * v.w);
+    l *= keep, o.x *= keep, o.y *= keep, o.z *= keep, o.w *= keep;
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      const float k = exp2_approx(ml[i].x - ref);
+      l = fmaf(k, ml[i].y, l);
+      o.x = fmaf(k, v[i].x, o.x), o.y = fmaf(k, v[i].y, o.y), o.z = fmaf(k, v[i].z, o.z), o.w = fmaf(k, v[i].w, o.w);
+    }
   }
   __device__ __forceinline__ float4 result() const {
     const float inv = l > 0.0f ? 1.0f / l : 0.0f;
@@ -191,8 +216,9 @@ struct KvSum {
 // the sequences' lengths, and works alone: it brings its groups by bulk copies
 // into a ring of its own, across the ends of items, and holds the running
 // maximum, sum and outputs of its keys. An item that one warp has whole is
-// finished there; the others' partial results are joined, in the block where
-// the item lies in it, else by a second launch.
+// finished there; the others' partial results are joined by the block that has
+// the item, or by the last of the item's blocks to be done (always in the
+// line's order: the same sums every time).
 //
 // Products run on the tensor cores with the cached codes as exact fp16
 // integers. fp32 queries (FINE): eight rows fill a 16-row tile, rows 0..7 with
@@ -211,10 +237,16 @@ __device__ __forceinline__ void kv_attn_body(const KvLaunch &p, uint32_t *status
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ __align__(8) uint64_t bars[NW * S];
   __shared__ int64_t scan[kThreads + 1];
+  // A partial result: groups [a, b) of an item's n; its maxima and sums are in
+  // piece_ml, its outputs in the warp's own shared memory if they are the warp's
+  // last, else in the scratch.
   struct Piece {
     int seq, head, tile, a, b, n;
+    const float *out;
   };
   __shared__ Piece pieces[2 * NW];
+  __shared__ float2 piece_ml[2 * NW][C::kRows];
+  __shared__ int last_block;
 
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, t = lane & 3;
   const KvMagic magic = p.magic;
@@ -232,48 +264,60 @@ __device__ __forceinline__ void kv_attn_body(const KvLaunch &p, uint32_t *status
   pdl_launch_dependents();
   pdl_wait();
 
-  // The line: scan[i] is where the sequences of thread i begin on it.
+  // The line: scan[i] is where the sequences of thread i begin on it. Up to 32
+  // sequences every warp sees for itself.
   const int64_t per_seq = static_cast<int64_t>(p.f.heads) * p.tiles;
   const int chunk = (p.a.batch + kThreads - 1) / kThreads;
+  int64_t total;
   {
-    const int s0 = min(p.a.batch, tid * chunk), s1 = min(p.a.batch, s0 + chunk);
+    const bool few = p.a.batch <= 32;
+    const int at = few ? lane : tid, s0 = min(p.a.batch, at * chunk), s1 = min(p.a.batch, s0 + chunk);
     int64_t incl = 0;
+    bool none = false;
     for (int s = s0; s < s1; ++s) {
-      const KvSeq q = kv_seq(p, s, status);
-      incl += kv_units(q.n) * per_seq;
+      const int n = kv_seq(p, s, status).n;
+      incl += kv_units(n) * per_seq;
+      none |= n == 0;
     }
     for (int o = 1; o < 32; o <<= 1) {
       const int64_t v = __shfl_up_sync(0xffffffffu, incl, o);
       if (lane >= o) incl += v;
     }
-    scan[tid + 1] = incl;
-    if (tid == 0) scan[0] = 0;
-    __syncthreads();
-    int64_t before = 0;
-    for (int w = 0; w < warp; ++w) before += scan[w * 32 + 32];
-    __syncthreads();
-    scan[tid + 1] = incl + before;
-    __syncthreads();
-  }
-  const int64_t total = scan[kThreads];
-
-  // Rows of sequences without keys.
-  for (int s = blockIdx.x; s < p.a.batch; s += gridDim.x) {
-    if (kv_seq(p, s, status).n) continue;
-    const int64_t n = static_cast<int64_t>(p.a.m) * p.a.hq * D;
-    for (int64_t e = tid * 4; e < n; e += kThreads * 4) kv_store(p, s * n + e, make_float4(0.f, 0.f, 0.f, 0.f));
+    if (few) {
+      total = __shfl_sync(0xffffffffu, incl, 31);
+      none = __any_sync(0xffffffffu, none);
+      if (warp == 0) scan[lane + 1] = incl;
+      if (tid == 0) scan[0] = 0;
+      if (tid >= 32) scan[tid + 1] = total;
+      __syncthreads();
+    } else {
+      scan[tid + 1] = incl;
+      if (tid == 0) scan[0] = 0;
+      none = __syncthreads_or(none);
+      int64_t before = 0;
+      for (int w = 0; w < warp; ++w) before += scan[w * 32 + 32];
+      __syncthreads();
+      scan[tid + 1] = incl + before;
+      __syncthreads();
+      total = scan[kThreads];
+    }
+    if (none)  // rows of sequences without keys
+      for (int s = blockIdx.x; s < p.a.batch; s += gridDim.x) {
+        if (kv_seq(p, s, status).n) continue;
+        const int64_t n = static_cast<int64_t>(p.a.m) * p.a.hq * D;
+        for (int64_t e = tid * 4; e < n; e += kThreads * 4) kv_store(p, s * n + e, make_float4(0.f, 0.f, 0.f, 0.f));
+      }
   }
 
   // Blocks that work, this block's run of the line, and this warp's part of it.
   const int64_t least = static_cast<int64_t>(p.min_units) * NW;
-  const int64_t blocks = min(static_cast<int64_t>(gridDim.x), (total + least - 1) / least);
-  KvSplit *splits = reinterpret_cast<KvSplit *>(p.a.ws);
+  const int64_t blocks = min(static_cast<int64_t>(gridDim.x), kv_muldiv(total + least - 1, 1, least));
+  unsigned long long *counters = reinterpret_cast<unsigned long long *>(p.a.ws);
   constexpr int64_t kSlot = kv_attn_slot_floats(C::kRows, D);
   float *block_slots = p.a.ws + kKvMaxBlocks * 4 + 2 * blockIdx.x * kSlot;
-  float *warp_slots = p.a.ws + kKvMaxBlocks * (4 + 2 * kSlot) + 2 * NW * blockIdx.x * kSlot;
-  if (tid == 0) splits[blockIdx.x].seq = -1;
+  float *warp_slots = p.a.ws + kKvMaxBlocks * (4 + 2 * kSlot) + 2 * NW * blockIdx.x * C::kRows * D;
   if (blockIdx.x >= blocks) return;
-  const int64_t from = blockIdx.x * total / blocks, span = (blockIdx.x + 1) * total / blocks - from;
+  const int64_t from = kv_muldiv(blockIdx.x, total, blocks), span = kv_muldiv(blockIdx.x + 1, total, blocks) - from;
 
   // A warp's place on the line: an item's groups [a, b) of n, and the units behind them.
   struct Place {
@@ -314,7 +358,7 @@ __device__ __forceinline__ void kv_attn_body(const KvLaunch &p, uint32_t *status
   };
   Place use{};
   {
-    const int64_t pos = from + span * warp / NW;
+    const int64_t pos = from + span * warp / NW;  // (NW is a power of two)
     use.left = from + span * (warp + 1) / NW - pos;
     if (use.left > 0) {
       int lo = 0, hi = kThreads;  // scan[lo] <= pos < scan[hi]
@@ -334,7 +378,7 @@ __device__ __forceinline__ void kv_attn_body(const KvLaunch &p, uint32_t *status
         look(use);
       }
       const int64_t units = kv_units(use.n);
-      const int item = static_cast<int>((pos - base) / units);
+      const int item = static_cast<int>(kv_muldiv(pos - base, 1, units));
       use.head = item / p.tiles;
       use.tile = item - use.head * p.tiles;
       enter(use, pos - base - item * units);
@@ -392,30 +436,15 @@ __device__ __forceinline__ void kv_attn_body(const KvLaunch &p, uint32_t *status
     }
   };
 
-  window();
-  for (int i = 0; i < S; ++i) fill();
-
-  while (use.a < use.b && !dead) {
-    float top[OCT], sum[OCT];  // of rows 8 o + g
-    float2 acc[OCT][NB * 4];
-    int last[OCT], low[OCT];
-    float factor[OCT];
-
-    // ---- query rows as fragments ----
-    // Each row is brought to [2^14, 2^15) by a power of two so that both terms
-    // stay in fp16's range; its inverse, with the softmax's scale and log2(e),
-    // is the factor of the row's scores, positive: the scale's sign goes into
-    // the row.
-    __syncwarp();
+  // The query rows 8 o + g of an item, four dims of each half block a lane.
+  auto load_rows = [&](float4 (&rows)[OCT][NB][2]) {
 #pragma unroll
     for (int o = 0; o < OCT; ++o) {
       const int row = use.tile * C::kRows + o * 8 + g;
       const bool there = row < p.rows;
-      const int i = min(row / p.ratio, p.a.m - 1), h = there ? row - i * p.ratio : 0;
+      const int i = there ? row / p.ratio : 0, h = there ? row - i * p.ratio : 0;
       const int64_t at = use.seq * p.a.q_seq + i * p.a.q_tok +
                          (static_cast<int64_t>(use.head) * p.ratio + h) * p.a.q_head + 4 * t;
-      float4 x[NB][2];
-      float big = 0.0f;
 #pragma unroll
       for (int b = 0; b < NB; ++b)
 #pragma unroll
@@ -431,8 +460,41 @@ __device__ __forceinline__ void kv_attn_body(const KvLaunch &p, uint32_t *status
                               __uint_as_float(w.y << 16), __uint_as_float(w.y & 0xffff0000u));
             }
           }
+          rows[o][b][half] = v;
+        }
+    }
+  };
+
+  bool begun = false;
+  while (use.a < use.b) {
+    float4 rows[OCT][NB][2];
+    load_rows(rows);
+    if (!begun) {  // the first copies while the rows are on their way
+      window();
+      for (int i = 0; i < S; ++i) fill();
+      begun = true;
+    }
+    float top[OCT], sum[OCT];  // of rows 8 o + g
+    float2 acc[OCT][NB * 4];
+    int last[OCT], low[OCT];
+    float factor[OCT];
+
+    // ---- query rows as fragments ----
+    // Each row is brought to [2^14, 2^15) by a power of two so that both terms
+    // stay in fp16's range; its inverse, with the softmax's scale and log2(e),
+    // is the factor of the row's scores, positive: the scale's sign goes into
+    // the row.
+    __syncwarp();
+#pragma unroll
+    for (int o = 0; o < OCT; ++o) {
+      const int i = min((use.tile * C::kRows + o * 8 + g) / p.ratio, p.a.m - 1);
+      float big = 0.0f;
+#pragma unroll
+      for (int b = 0; b < NB; ++b)
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {
+          const float4 v = rows[o][b][half];
           big = fmaxf(big, fmaxf(fmaxf(fabsf(v.x), fabsf(v.y)), fmaxf(fabsf(v.z), fabsf(v.w))));
-          x[b][half] = v;
         }
       big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, 1));
       big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, 2));
@@ -447,7 +509,7 @@ __device__ __forceinline__ void kv_attn_body(const KvLaunch &p, uint32_t *status
       for (int b = 0; b < NB; ++b)
 #pragma unroll
         for (int half = 0; half < 2; ++half) {
-          const float4 v = x[b][half];
+          const float4 v = rows[o][b][half];
           const float2 even = make_float2(v.x * up, v.z * up), odd = make_float2(v.y * up, v.w * up);
           uint32_t *f = reinterpret_cast<uint32_t *>(qfrag + (((FINE ? o : o / 2) * NB + b) * 2 + half) * 32 + lane);
           if (FINE) {
@@ -473,10 +535,11 @@ __device__ __forceinline__ void kv_attn_body(const KvLaunch &p, uint32_t *status
     const int grp_end = use.first + use.b;
     int up_exp = 13;  // acc and sum are 2^up_exp and 2^13 times the outputs' and weights' sums
 
-    for (int grp = use.first + use.a; grp < grp_end; grp += TG) {
+    for (int grp = use.first + use.a; grp < grp_end && !dead; grp += TG) {
       const int st = used % S;
       if (!__all_sync(0xffffffffu, mbar_wait(bar + st, (used / S) & 1))) {
-        // Nothing more is copied; what is in flight is waited for once more.
+        // Nothing more is copied; what is in flight is waited for once more. The
+        // warp's items end with what they have, so that no block waits in vain.
         bool drained = true;
         for (uint32_t i = used; i != filled; ++i) drained = mbar_wait(bar + i % S, (i / S) & 1) && drained;
         if (lane == 0) atomicOr(status, kDevTimeoutFull | (drained ? 0u : kDevTimeoutDrain));
@@ -747,24 +810,27 @@ __device__ __forceinline__ void kv_attn_body(const KvLaunch &p, uint32_t *status
       __syncwarp();  // every lane has read the stage
       fill();
     }
-    if (dead) break;
 
     // ---- the item's end for this warp ----
     const bool whole = use.a == 0 && use.b == use.n;
     const float down = __uint_as_float(static_cast<uint32_t>(127 - up_exp) << 23);
-    float *slot = warp_slots + (2 * warp + (use.a == 0 ? 1 : 0)) * kSlot;
-    if (!whole && lane == 0) pieces[2 * warp + (use.a == 0 ? 1 : 0)] = Piece{use.seq, use.head, use.tile, use.a, use.b, use.n};
+    const int piece = 2 * warp + (use.a == 0 ? 1 : 0);
+    const Place done = use;
+    next(use);
+    float *kept = use.a == use.b ? reinterpret_cast<float *>(own) : warp_slots + piece * C::kRows * D;
+    if (!whole && lane == 0) pieces[piece] = Piece{done.seq, done.head, done.tile, done.a, done.b, done.n, kept};
+    __syncwarp();
 #pragma unroll
     for (int o = 0; o < OCT; ++o) {
       float l = sum[o] * 0x1p-13f;
       l += __shfl_xor_sync(0xffffffffu, l, 1);
       l += __shfl_xor_sync(0xffffffffu, l, 2);
-      const int row = use.tile * C::kRows + o * 8 + g;
+      const int row = done.tile * C::kRows + o * 8 + g;
       if (row >= p.rows) continue;
       const float by = whole ? (l > 0.0f ? down / l : 0.0f) : down;
-      const int64_t out = kv_out_at(p, use.seq, use.head, row, D);
-      float *part = slot + (o * 8 + g) * D;
-      if (!whole && t == 0) *reinterpret_cast<float2 *>(slot + C::kRows * D + (o * 8 + g) * 2) = make_float2(top[o], l);
+      const int64_t out = kv_out_at(p, done.seq, done.head, row, D);
+      float *part = kept + (o * 8 + g) * D;
+      if (!whole && t == 0) piece_ml[piece][o * 8 + g] = make_float2(top[o], l);
 #pragma unroll
       for (int b = 0; b < NB; ++b)
 #pragma unroll
@@ -778,7 +844,6 @@ __device__ __forceinline__ void kv_attn_body(const KvLaunch &p, uint32_t *status
             *reinterpret_cast<float4 *>(part + d) = v;
         }
     }
-    next(use);
   }
 
   // ---- the block's partial results, in the line's order ----
@@ -801,11 +866,19 @@ __device__ __forceinline__ void kv_attn_body(const KvLaunch &p, uint32_t *status
       const int r = i / (D / 4), d = (i - r * (D / 4)) * 4, row = first.tile * C::kRows + r;
       if (row >= p.rows) continue;
       KvSum x;
-      for (int k = e; k < stop; ++k) {
-        if (pieces[k].seq < 0) continue;
-        const float *s = warp_slots + k * kSlot;
-        const float2 ml = *reinterpret_cast<const float2 *>(s + C::kRows * D + r * 2);
-        x.add(ml.x, ml.y, *reinterpret_cast<const float4 *>(s + r * D + d));
+      for (int k = e; k < stop; k += 4) {
+        float2 ml[4];
+        float4 v[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          ml[j] = make_float2(-INFINITY, 0.0f);
+          v[j] = make_float4(0.f, 0.f, 0.f, 0.f);
+          if (k + j < stop && pieces[min(k + j, 2 * NW - 1)].seq >= 0) {
+            ml[j] = piece_ml[k + j][r];
+            v[j] = *reinterpret_cast<const float4 *>(pieces[k + j].out + r * D + d);
+          }
+        }
+        x.add(ml, v);
       }
       if (whole) {
         kv_store(p, kv_out_at(p, first.seq, first.head, row, D) + d, x.result());
@@ -814,12 +887,52 @@ __device__ __forceinline__ void kv_attn_body(const KvLaunch &p, uint32_t *status
         if (d == 0) *reinterpret_cast<float2 *>(slot + C::kRows * D + r * 2) = make_float2(x.m, x.l);
       }
     }
-    if (!whole && first.a == 0 && tid == 0) {
-      // The item's last unit on the line, and the block that holds it.
+    if (!whole) {
+      // The item's blocks: those of its first group and of its last unit.
       int64_t at = scan[first.seq / chunk];
       for (int s = first.seq / chunk * chunk; s < first.seq; ++s) at += kv_units(kv_seq(p, s, status).n) * per_seq;
-      at += (static_cast<int64_t>(first.head) * p.tiles + first.tile + 1) * kv_units(first.n) - 1;
-      splits[blockIdx.x] = KvSplit{first.seq, first.head, first.tile, static_cast<int>(((at + 1) * blocks - 1) / total)};
+      at += (static_cast<int64_t>(first.head) * p.tiles + first.tile) * kv_units(first.n);
+      const int b0 = kv_block_of(at + kKvItemCost, blocks, total);
+      const int b1 = kv_block_of(at + kv_units(first.n) - 1, blocks, total);
+      __threadfence();
+      __syncthreads();
+      if (tid == 0) {
+        // Counters need no first value: one that another call left has another epoch.
+        unsigned long long *counter = counters + b0, seen = *reinterpret_cast<volatile unsigned long long *>(counter), now;
+        do {
+          now = seen;
+          const unsigned long long count = (now >> 16) == p.epoch ? now : p.epoch << 16;
+          seen = atomicCAS(counter, now, count + 1);
+          last_block = static_cast<int>(count & 0xffff) == b1 - b0;
+        } while (seen != now);
+        if (last_block) *reinterpret_cast<volatile unsigned long long *>(counter) = p.epoch << 16;  // for a replay
+        __threadfence();
+      }
+      __syncthreads();
+      if (last_block) {
+        const float *parts = p.a.ws + kKvMaxBlocks * 4;
+        for (int i = tid; i < C::kRows * (D / 4); i += kThreads) {
+          const int r = i / (D / 4), d = (i - r * (D / 4)) * 4, row = first.tile * C::kRows + r;
+          if (row >= p.rows) continue;
+          KvSum x;
+          for (int k = b0; k <= b1; k += 8) {  // slot 1 of the first block, slot 0 of the others
+            float2 ml[8];
+            float4 v[8];
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+              ml[j] = make_float2(-INFINITY, 0.0f);
+              v[j] = make_float4(0.f, 0.f, 0.f, 0.f);
+              if (k + j <= b1) {
+                const float *s = parts + (2 * (k + j) + (k + j == b0 ? 1 : 0)) * kSlot;
+                ml[j] = __ldcg(reinterpret_cast<const float2 *>(s + C::kRows * D + r * 2));
+                v[j] = __ldcg(reinterpret_cast<const float4 *>(s + r * D + d));
+              }
+            }
+            x.add(ml, v);
+          }
+          kv_store(p, kv_out_at(p, first.seq, first.head, row, D) + d, x.result());
+        }
+      }
     }
     e = stop;
   }
