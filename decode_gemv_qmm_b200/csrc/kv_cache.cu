@@ -2,14 +2,15 @@
 // tokens back (include/qmm.h, "Quantised key/value cache"; kv_layout.cuh).
 //
 // Both move bytes: a row of D elements against its D/2 + D/16 (Q4_0) or D + D/16
-// (Q8_0) bytes, with a few operations an element, so memory bounds them once
-// every load and store is wide and many are in flight. A thread takes one eighth
-// of a 32-block, dims 4q .. 4q+3 and 16+4q .. 16+4q+3 (q < 4): two vectors of
-// four elements in the rows, and in the cache one word (keys, Q4_0), two words
-// that follow each other (keys, Q8_0) or the same bytes in two places (values);
-// the four threads of a block follow each other, the blocks of a row too, so a
-// warp's accesses fill whole sectors on either side. Keys and values are the two
-// halves of the grid: a warp has one kind only.
+// (Q8_0) bytes, with a few operations an element. A thread takes quarter q of a
+// run of blocks (kv_layout.cuh): dims 4q .. 4q+3 and 16+4q .. 16+4q+3 of its 4, 2
+// or 1 blocks, which are up to 16 bytes that follow each other in the cache, for
+// keys and for values; the four quarters of a run follow each other, so a warp's
+// accesses fill whole sectors on either side. Its head, run and quarter stay the
+// same over its tokens, so a token costs an address and the conversions (one
+// eighth of a block a thread, with every address worked out anew, took 130 us
+// where this takes 64 us for 65536 tokens, 8 heads of 128, Q4_0, bf16). Keys
+// and values are the two halves of the grid.
 #include <algorithm>
 
 #include "kv_layout.cuh"
@@ -39,179 +40,282 @@ struct KvRows {
   int64_t tok, head;  // strides in elements
 };
 
-// What a thread works on: eighth q of block b of the row (token, head).
-struct KvItem {
-  int64_t tok;
-  int head, b, q;
+// Blocks of a launch for each SM (65536 tokens read: 90 us with 2, 67 with 8, 64 with 16).
+constexpr int kKvBlocks = 16;
+
+// Runs of blocks of a row.
+constexpr int kv_runs(int nb, bool q8) { return q8 ? nb / 2 + nb % 2 : nb / 4 + nb % 4 / 2 + nb % 2; }
+
+// What a thread works on, the same for all its tokens: quarter q of a run of a head.
+struct KvUnit {
+  int head, q, first, n;  // the run's first block, its blocks
+  int64_t tok, step;      // the thread's first token, and how far the next one is
+  bool there;
 };
 
-template <int NB>
-__device__ __forceinline__ KvItem item_of(int64_t i, int heads) {
-  KvItem it;
-  it.q = static_cast<int>(i & 3);
-  const int64_t block = i >> 2, row = block / NB;
-  it.b = static_cast<int>(block - row * NB);
-  it.tok = row / heads;
-  it.head = static_cast<int>(row - it.tok * heads);
-  return it;
+// Units of a token lie on the threads of a block, as many tokens as fit; where
+// one token's do not fit, the grid's z counts blocks of them.
+template <int NB, bool Q8>
+__device__ __forceinline__ KvUnit unit_of(int heads) {
+  constexpr int kRuns = kv_runs(NB, Q8);
+  const int units = heads * kRuns * 4, per = units <= 256 ? 256 / units : 1;
+  const int tid = threadIdx.x, slot = units <= 256 ? tid / units : 0;
+  const int u = units <= 256 ? tid - slot * units : blockIdx.z * 256 + tid;
+  KvUnit k;
+  k.q = u & 3;
+  const int run = (u >> 2) % kRuns;
+  k.head = (u >> 2) / kRuns;
+  k.first = run * (Q8 ? 2 : 4);
+  if (!Q8 && NB % 4 == 3 && run == kRuns - 1) k.first = NB - 1;
+  k.n = kv_run(NB, Q8, min(k.first, NB - 1)).n;
+  k.tok = static_cast<int64_t>(blockIdx.x) * per + slot;
+  k.step = static_cast<int64_t>(gridDim.x) * per;
+  k.there = slot < per && u < units && (units > 256 || blockIdx.z == 0);
+  return k;
 }
 
-// The part (keys' or values') of the group that a slot's token lies in, and its
-// place there; nullptr for a slot that is left out (negative) or does not exist
-// (recorded).
-__device__ __forceinline__ uint8_t *part_of(const KvForm &f, uint8_t *cache, int64_t slot, int head, bool val, int *place) {
-  if (slot < 0) return nullptr;
+// Where a token's bytes of a unit are: the part of its group, and its place there.
+// False for a slot that is left out (negative) or does not exist (recorded).
+struct KvAt {
+  int64_t part;
+  int place;
+};
+__device__ __forceinline__ bool at_slot(const KvForm &f, int64_t slot, int head, bool val, KvAt *at) {
+  if (slot < 0) return false;
   const int shift = 31 - __clz(f.page);
   const int64_t pg = slot >> shift;
   if (pg >= f.pages) {
     atomicOr(&g_kv_status, kDevBadIndex);
-    return nullptr;
+    return false;
   }
-  const int in = static_cast<int>(slot & (f.page - 1));
-  *place = in % kKvGroup;
-  return cache + f.group_at(pg, head, in / kKvGroup) + (val ? kv_part_bytes(f.nb, f.kq8) : 0);
+  const int in = static_cast<int>(slot) & (f.page - 1);
+  at->place = in % kKvGroup;
+  at->part = f.group_at(pg, head, in / kKvGroup) + (val ? kv_part_bytes(f.nb, f.kq8) : 0);
+  return true;
 }
 
-// Offsets of the eighth's bytes: `at`, and for values (the second half of the
-// four dims) `at + next`.
-template <int NB>
-__device__ __forceinline__ int bytes_of(bool q8, bool val, int place, int b, int q, int *next) {
-  const KvRun r = kv_run(NB, q8, b);
-  if (!val) {
-    const int row = 8 * (place >> 3) + 2 * (place & 3) + ((place >> 2) & 1), unit = q8 ? 8 : 4;
-    *next = 4;
-    return r.first * unit * 64 + ((row * 4 + q) * r.n + b - r.first) * unit;
-  }
-  const int unit = q8 ? 4 : 2, g = 2 * q;
-  const bool halves = r.n * unit == 8;
-  *next = r.n * unit;
-  return r.first * unit * 128 + (halves ? ((g >> 2) * 64 + place * 4 + (g & 3)) * 8 : (place * 8 + g) * r.n * unit) +
-         (b - r.first) * unit;
+// Offset in the part of a unit's bytes, n * (Q8 ? 8 : 4) of them.
+template <bool Q8>
+__device__ __forceinline__ int unit_at(const KvUnit &k, bool val, int place) {
+  constexpr int kBytes = Q8 ? 8 : 4;  // of a quarter block
+  const int base = k.first * kBytes * 64;
+  if (!val) return base + ((8 * (place >> 3) + 2 * (place & 3) + ((place >> 2) & 1)) * 4 + k.q) * k.n * kBytes;
+  if (k.n * kBytes == 16) return base + ((k.q >> 1) * 32 + place * 2 + (k.q & 1)) * 16;
+  return base + (place * 4 + k.q) * k.n * kBytes;
 }
 
-// Four codes as bytes of a word.
-__device__ __forceinline__ uint32_t pack4(const int *c) {
-  return (c[0] & 0xff) | (c[1] & 0xff) << 8 | (c[2] & 0xff) << 16 | static_cast<uint32_t>(c[3] & 0xff) << 24;
+// A unit's words, by blocks: Q4_0 one of a block (low nibbles dims 4q + e, high
+// ones 16 + 4q + e, byte e), Q8_0 two (dims 4q + e; 16 + 4q + e). Values lie by
+// pairs of dims, so the halves of two words are exchanged, either way.
+template <bool Q8>
+__device__ __forceinline__ void by_blocks(uint32_t (&w)[4], int n, bool val) {
+  if (!val) return;
+  const uint32_t a = w[0], b = w[1], c = w[2], d = w[3];
+  if (Q8) {
+    if (n == 2)
+      w[0] = __byte_perm(a, c, 0x5410), w[1] = __byte_perm(a, c, 0x7632), w[2] = __byte_perm(b, d, 0x5410), w[3] = __byte_perm(b, d, 0x7632);
+    else
+      w[0] = __byte_perm(a, b, 0x5410), w[1] = __byte_perm(a, b, 0x7632);
+  } else if (n == 4) {
+    w[0] = __byte_perm(a, c, 0x5410), w[1] = __byte_perm(a, c, 0x7632), w[2] = __byte_perm(b, d, 0x5410), w[3] = __byte_perm(b, d, 0x7632);
+  } else if (n == 2) {
+    w[0] = __byte_perm(a, b, 0x5410), w[1] = __byte_perm(a, b, 0x7632);
+  }
+}
+template <bool Q8>
+__device__ __forceinline__ void by_pairs(uint32_t (&w)[4], int n, bool val) {
+  if (!val) return;
+  const uint32_t a = w[0], b = w[1], c = w[2], d = w[3];
+  if (n == (Q8 ? 2 : 4))
+    w[0] = __byte_perm(a, b, 0x5410), w[2] = __byte_perm(a, b, 0x7632), w[1] = __byte_perm(c, d, 0x5410), w[3] = __byte_perm(c, d, 0x7632);
+  else if (Q8 || n == 2)
+    w[0] = __byte_perm(a, b, 0x5410), w[1] = __byte_perm(a, b, 0x7632);
+}
+
+template <int NB, bool Q8, typename T>
+__device__ __forceinline__ void write_units(const KvForm &f, int64_t tokens, const T *rows, KvRows st, bool val,
+                                            const int64_t *slots, uint8_t *cache) {
+  constexpr int kMost = Q8 ? 2 : 4;  // blocks of a unit
+  const KvUnit k = unit_of<NB, Q8>(f.heads);
+  // whole warps take part in a round: the four quarters of a run are in one
+  const int64_t rounds = (tokens + k.step - 1) / k.step;
+  int64_t tok = k.tok;
+  for (int64_t i = 0; i < rounds; ++i, tok += k.step) {
+    const bool there = k.there && tok < tokens;
+    const int64_t slot = there ? __ldg(slots + tok) : -1;
+    float x[kMost][8];
+    const T *row = rows + tok * st.tok + k.head * st.head + k.first * 32 + k.q * 4;
+#pragma unroll
+    for (int j = 0; j < kMost; ++j) {
+      float4 lo = make_float4(0.f, 0.f, 0.f, 0.f), hi = lo;
+      if (there && j < k.n) lo = load4(row + j * 32), hi = load4(row + j * 32 + 16);
+      x[j][0] = lo.x, x[j][1] = lo.y, x[j][2] = lo.z, x[j][3] = lo.w;
+      x[j][4] = hi.x, x[j][5] = hi.y, x[j][6] = hi.z, x[j][7] = hi.w;
+    }
+    // The blocks' extremes, over the four quarters: for Q8_0 the largest
+    // magnitude, for Q4_0 the value that has it (of two, the first).
+    float top[kMost];
+    bool tie = false;
+#pragma unroll
+    for (int j = 0; j < kMost; ++j) {
+      float up = Q8 ? fabsf(x[j][0]) : x[j][0], down = x[j][0];
+#pragma unroll
+      for (int e = 1; e < 8; ++e) {
+        up = fmaxf(up, Q8 ? fabsf(x[j][e]) : x[j][e]);
+        if (!Q8) down = fminf(down, x[j][e]);
+      }
+      up = fmaxf(up, __shfl_xor_sync(0xffffffffu, up, 1));
+      up = fmaxf(up, __shfl_xor_sync(0xffffffffu, up, 2));
+      if (!Q8) {
+        down = fminf(down, __shfl_xor_sync(0xffffffffu, down, 1));
+        down = fminf(down, __shfl_xor_sync(0xffffffffu, down, 2));
+        tie |= up == -down && up != 0.0f;
+      }
+      top[j] = Q8 || up >= -down ? up : down;
+    }
+    if (!Q8 && __any_sync(0xffffffffu, tie)) {
+#pragma unroll
+      for (int j = 0; j < kMost; ++j) {  // the least of 2 dim + sign
+        uint32_t first = 64;
+#pragma unroll
+        for (int e = 7; e >= 0; --e)
+          if (fabsf(x[j][e]) == fabsf(top[j])) first = 2 * ((e & 4) * 4 + k.q * 4 + (e & 3)) + (__float_as_uint(x[j][e]) >> 31);
+        first = min(first, __shfl_xor_sync(0xffffffffu, first, 1));
+        first = min(first, __shfl_xor_sync(0xffffffffu, first, 2));
+        top[j] = first & 1 ? -fabsf(top[j]) : fabsf(top[j]);
+      }
+    }
+    // Quarter j works out block j's scale and its inverse for all four.
+    float mine = top[0];
+#pragma unroll
+    for (int j = 1; j < kMost; ++j)
+      if (k.q == j) mine = top[j];
+    const float scale = Q8 ? __fdiv_rn(mine, 127.0f) : mine * -0.125f;
+    const float inverse = scale != 0.0f ? __fdiv_rn(1.0f, scale) : 0.0f;
+    uint32_t w[4];
+#pragma unroll
+    for (int j = 0; j < kMost; ++j) {
+      const float id = __shfl_sync(0xffffffffu, inverse, (threadIdx.x & 28) + j);
+      uint32_t c[8];
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        const float y = __fmul_rn(x[j][e], id);
+        if (Q8)  // half away from zero: the number below 0.5 takes halves up and nothing else; |y| < 127.5
+          c[e] = static_cast<uint32_t>(__float2int_rz(__fadd_rn(y, copysignf(0.49999997f, y))));
+        else  // truncated: the sum with 2^23, rounded towards zero, ends in the code
+          c[e] = __float_as_uint(__fadd_rz(fminf(__fadd_rn(y, 8.5f), 15.5f), 8388608.0f));
+      }
+      const uint32_t lo = __byte_perm(__byte_perm(c[0], c[1], 0x0040), __byte_perm(c[2], c[3], 0x0040), 0x5410);
+      const uint32_t hi = __byte_perm(__byte_perm(c[4], c[5], 0x0040), __byte_perm(c[6], c[7], 0x0040), 0x5410);
+      if (Q8)
+        w[(2 * j) & 3] = lo, w[(2 * j + 1) & 3] = hi;
+      else
+        w[j & 3] = (lo & 0x0f0f0f0fu) | (hi << 4 & 0xf0f0f0f0u);
+    }
+    KvAt at;
+    if (!there || !at_slot(f, slot, k.head, val, &at)) continue;
+    uint8_t *part = cache + at.part, *to = part + unit_at<Q8>(k, val, at.place);
+    by_pairs<Q8>(w, k.n, val);
+    if (k.n == kMost)
+      *reinterpret_cast<uint4 *>(to) = make_uint4(w[0], w[1], w[2], w[3]);
+    else if (Q8 || k.n == 2)
+      *reinterpret_cast<uint2 *>(to) = make_uint2(w[0], w[1]);
+    else
+      *reinterpret_cast<uint32_t *>(to) = w[0];
+    if (k.q < k.n)
+      *reinterpret_cast<uint16_t *>(part + kv_scale_at(NB, Q8, at.place, k.first + k.q)) =
+          __half_as_ushort(__float2half_rn(scale));
+  }
+}
+
+template <int NB, bool Q8, typename T>
+__device__ __forceinline__ void read_units(const KvForm &f, int64_t tokens, T *rows, bool val, const int64_t *slots,
+                                           const uint8_t *cache) {
+  constexpr int kMost = Q8 ? 2 : 4;
+  const KvUnit k = unit_of<NB, Q8>(f.heads);
+  if (!k.there) return;
+  int64_t slot = k.tok < tokens ? __ldg(slots + k.tok) : -1;
+  for (int64_t tok = k.tok; tok < tokens; tok += k.step) {
+    const int64_t now = slot;
+    if (tok + k.step < tokens) slot = __ldg(slots + tok + k.step);
+    KvAt at;
+    if (!at_slot(f, now, k.head, val, &at)) continue;
+    const uint8_t *part = cache + at.part, *from = part + unit_at<Q8>(k, val, at.place);
+    uint32_t w[4] = {0u, 0u, 0u, 0u};
+    if (k.n == kMost) {
+      const uint4 v = *reinterpret_cast<const uint4 *>(from);
+      w[0] = v.x, w[1] = v.y, w[2] = v.z, w[3] = v.w;
+    } else if (Q8 || k.n == 2) {
+      const uint2 v = *reinterpret_cast<const uint2 *>(from);
+      w[0] = v.x, w[1] = v.y;
+    } else {
+      w[0] = *reinterpret_cast<const uint32_t *>(from);
+    }
+    float d[kMost];
+#pragma unroll
+    for (int j = 0; j < kMost; ++j)
+      d[j] = j < k.n ? half_bits_to_float(*reinterpret_cast<const uint16_t *>(part + kv_scale_at(NB, Q8, at.place, k.first + j)))
+                     : 0.0f;
+    by_blocks<Q8>(w, k.n, val);
+    T *row = rows + (tok * f.heads + k.head) * (NB * 32) + k.first * 32 + k.q * 4;
+#pragma unroll
+    for (int j = 0; j < kMost; ++j) {
+      if (j >= k.n) continue;
+      float x[8];
+      if (Q8) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {  // 2^23 + 128 + c, from the byte c + 128
+          x[e] = __uint_as_float(__byte_perm(w[(2 * j) & 3] ^ 0x80808080u, 0x4b000000u, 0x7440 + e)) - 8388736.0f;
+          x[e + 4] = __uint_as_float(__byte_perm(w[(2 * j + 1) & 3] ^ 0x80808080u, 0x4b000000u, 0x7440 + e)) - 8388736.0f;
+        }
+      } else {
+        const uint32_t lo = w[j & 3] & 0x0f0f0f0fu, hi = w[j & 3] >> 4 & 0x0f0f0f0fu;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {  // 2^23 + c
+          x[e] = __uint_as_float(__byte_perm(lo, 0x4b000000u, 0x7440 + e)) - 8388616.0f;
+          x[e + 4] = __uint_as_float(__byte_perm(hi, 0x4b000000u, 0x7440 + e)) - 8388616.0f;
+        }
+      }
+      store4(row + j * 32, make_float4(x[0] * d[j], x[1] * d[j], x[2] * d[j], x[3] * d[j]));
+      store4(row + j * 32 + 16, make_float4(x[4] * d[j], x[5] * d[j], x[6] * d[j], x[7] * d[j]));
+    }
+  }
 }
 
 template <int NB, typename T>
-__global__ void __launch_bounds__(256) kv_write_kernel(KvForm f, int64_t items, const T *K, KvRows ks, const T *V,
+__global__ void __launch_bounds__(256) kv_write_kernel(KvForm f, int64_t tokens, const T *K, KvRows ks, const T *V,
                                                        KvRows vs, const int64_t *slots, uint8_t *cache) {
   pdl_launch_dependents();
   pdl_wait();
   const bool val = blockIdx.y;
-  const bool q8 = val ? f.vq8 : f.kq8;
-  const T *rows = val ? V : K;
-  const KvRows st = val ? vs : ks;
-  const int64_t step = static_cast<int64_t>(gridDim.x) * blockDim.x;
-  // whole warps take part in a round: the four threads of a block are in one
-  for (int64_t i = static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x; i - (threadIdx.x & 31) < items; i += step) {
-    const bool there = i < items;
-    const KvItem it = item_of<NB>(there ? i : items - 1, f.heads);
-    const int64_t slot = __ldg(slots + it.tok);
-    const T *row = rows + it.tok * st.tok + it.head * st.head + it.b * 32 + it.q * 4;
-    const float4 lo = load4(row), hi = load4(row + 16);
-    const float x[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
-    float top = 0.0f;
-#pragma unroll
-    for (int j = 0; j < 8; ++j) top = fmaxf(top, fabsf(x[j]));
-    top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
-    top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
-    int c[8];
-    float d;
-    if (q8) {
-      d = __fdiv_rn(top, 127.0f);
-      const float id = d != 0.0f ? __fdiv_rn(1.0f, d) : 0.0f;
-#pragma unroll
-      for (int j = 0; j < 8; ++j)
-        c[j] = static_cast<int>(fminf(fmaxf(roundf(__fmul_rn(x[j], id)), -127.0f), 127.0f));
-    } else {
-      // the first of the largest gives the sign: the least of 2 dim + sign
-      uint32_t first = 64;
-#pragma unroll
-      for (int j = 7; j >= 0; --j)
-        if (fabsf(x[j]) == top) first = 2 * ((j & 4) * 4 + it.q * 4 + (j & 3)) + (__float_as_uint(x[j]) >> 31);
-      first = min(first, __shfl_xor_sync(0xffffffffu, first, 1));
-      first = min(first, __shfl_xor_sync(0xffffffffu, first, 2));
-      d = first & 1 ? top * 0.125f : top * -0.125f;
-      const float id = d != 0.0f ? __fdiv_rn(1.0f, d) : 0.0f;
-#pragma unroll
-      for (int j = 0; j < 8; ++j)
-        c[j] = static_cast<int>(fminf(fmaxf(__fadd_rn(__fmul_rn(x[j], id), 8.5f), 0.0f), 15.0f));
-#pragma unroll
-      for (int j = 0; j < 4; ++j) c[j] |= c[j + 4] << 4;
-    }
-    int place = 0;
-    uint8_t *part = there ? part_of(f, cache, slot, it.head, val, &place) : nullptr;
-    if (part == nullptr) continue;
-    int next;
-    uint8_t *at = part + bytes_of<NB>(q8, val, place, it.b, it.q, &next);
-    if (!val) {
-      if (q8)
-        *reinterpret_cast<uint2 *>(at) = make_uint2(pack4(c), pack4(c + 4));
-      else
-        *reinterpret_cast<uint32_t *>(at) = pack4(c);
-    } else if (q8) {
-      const int a[8] = {c[0], c[1], c[4], c[5], c[2], c[3], c[6], c[7]};
-      *reinterpret_cast<uint32_t *>(at) = pack4(a);
-      *reinterpret_cast<uint32_t *>(at + next) = pack4(a + 4);
-    } else {
-      const uint32_t w = pack4(c);
-      *reinterpret_cast<uint16_t *>(at) = static_cast<uint16_t>(w);
-      *reinterpret_cast<uint16_t *>(at + next) = static_cast<uint16_t>(w >> 16);
-    }
-    if (it.q == 0)
-      *reinterpret_cast<uint16_t *>(part + kv_scale_at(NB, q8, place, it.b)) = __half_as_ushort(__float2half_rn(d));
-  }
+  if (val ? f.vq8 : f.kq8)
+    write_units<NB, true>(f, tokens, val ? V : K, val ? vs : ks, val, slots, cache);
+  else
+    write_units<NB, false>(f, tokens, val ? V : K, val ? vs : ks, val, slots, cache);
 }
 
 template <int NB, typename T>
-__global__ void __launch_bounds__(256) kv_read_kernel(KvForm f, int64_t items, T *K, T *V, const int64_t *slots,
-                                                      uint8_t *cache) {
+__global__ void __launch_bounds__(256) kv_read_kernel(KvForm f, int64_t tokens, T *K, T *V, const int64_t *slots,
+                                                      const uint8_t *cache) {
   pdl_launch_dependents();
   pdl_wait();
   const bool val = blockIdx.y;
-  const bool q8 = val ? f.vq8 : f.kq8;
-  T *rows = val ? V : K;
-  const int64_t step = static_cast<int64_t>(gridDim.x) * blockDim.x;
-  for (int64_t i = static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x; i < items; i += step) {
-    const KvItem it = item_of<NB>(i, f.heads);
-    int place = 0, next;
-    const uint8_t *part = part_of(f, cache, __ldg(slots + it.tok), it.head, val, &place);
-    if (part == nullptr) continue;
-    const uint8_t *at = part + bytes_of<NB>(q8, val, place, it.b, it.q, &next);
-    const float d = half_bits_to_float(*reinterpret_cast<const uint16_t *>(part + kv_scale_at(NB, q8, place, it.b)));
-    float x[8];
-    if (q8) {
-      const uint32_t w0 = *reinterpret_cast<const uint32_t *>(at), w1 = *reinterpret_cast<const uint32_t *>(at + next);
-      // values: bytes are dims 0, 1, 16, 17 and 2, 3, 18, 19
-      const uint32_t lo = val ? __byte_perm(w0, w1, 0x5410) : w0, hi = val ? __byte_perm(w0, w1, 0x7632) : w1;
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        x[j] = static_cast<float>(static_cast<int8_t>(lo >> (8 * j)));
-        x[j + 4] = static_cast<float>(static_cast<int8_t>(hi >> (8 * j)));
-      }
-    } else {
-      const uint32_t w = val ? *reinterpret_cast<const uint16_t *>(at) |
-                                   static_cast<uint32_t>(*reinterpret_cast<const uint16_t *>(at + next)) << 16
-                             : *reinterpret_cast<const uint32_t *>(at);
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        x[j] = static_cast<float>(static_cast<int>(w >> (8 * j) & 15) - 8);
-        x[j + 4] = static_cast<float>(static_cast<int>(w >> (8 * j + 4) & 15) - 8);
-      }
-    }
-    T *row = rows + (it.tok * f.heads + it.head) * (NB * 32) + it.b * 32 + it.q * 4;
-    store4(row, make_float4(x[0] * d, x[1] * d, x[2] * d, x[3] * d));
-    store4(row + 16, make_float4(x[4] * d, x[5] * d, x[6] * d, x[7] * d));
-  }
+  if (val ? f.vq8 : f.kq8)
+    read_units<NB, true>(f, tokens, val ? V : K, val, slots, cache);
+  else
+    read_units<NB, false>(f, tokens, val ? V : K, val, slots, cache);
 }
 
-template <typename... P, typename... A>
-cudaError_t launch(const DevInfo &dev, int64_t items, cudaStream_t stream, void (*kernel)(P...), A... args) {
+template <int NB, typename... P, typename... A>
+cudaError_t launch(const DevInfo &dev, const KvForm &f, int64_t tokens, cudaStream_t stream, void (*kernel)(P...), A... args) {
+  // units of a token, by the type with the more of them (the other's blocks find none)
+  const int units = f.heads * 4 * kv_runs(NB, f.kq8 || f.vq8), most = std::min(kv_runs(NB, true), kv_runs(NB, false));
+  const int64_t per = std::max(1, 256 / (f.heads * 4 * (f.kq8 && f.vq8 ? kv_runs(NB, true) : most)));
   cudaLaunchConfig_t cfg{};
   cfg.blockDim = dim3(256);
-  cfg.gridDim = dim3(static_cast<unsigned>(std::min<int64_t>((items + 255) / 256, static_cast<int64_t>(dev.sms) * 4)), 2);
+  const int64_t want = (tokens + per - 1) / per, z = (units + 255) / 256;
+  cfg.gridDim = dim3(static_cast<unsigned>(std::min<int64_t>(want, std::max<int64_t>(1, dev.sms * kKvBlocks / z))), 2,
+                     static_cast<unsigned>(z));
   cfg.stream = stream;
   cudaLaunchAttribute attr;
   attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -222,17 +326,17 @@ cudaError_t launch(const DevInfo &dev, int64_t items, cudaStream_t stream, void 
 }
 
 template <int NB, typename T>
-cudaError_t write_rows(const DevInfo &dev, const KvForm &f, int64_t items, const void *K, KvRows ks, const void *V,
+cudaError_t write_rows(const DevInfo &dev, const KvForm &f, int64_t tokens, const void *K, KvRows ks, const void *V,
                        KvRows vs, const int64_t *slots, void *cache, cudaStream_t stream) {
-  return launch(dev, items, stream, kv_write_kernel<NB, T>, f, items, static_cast<const T *>(K), ks,
+  return launch<NB>(dev, f, tokens, stream, kv_write_kernel<NB, T>, f, tokens, static_cast<const T *>(K), ks,
                 static_cast<const T *>(V), vs, slots, static_cast<uint8_t *>(cache));
 }
 
 template <int NB, typename T>
-cudaError_t read_rows(const DevInfo &dev, const KvForm &f, int64_t items, const int64_t *slots, const void *cache, void *K,
+cudaError_t read_rows(const DevInfo &dev, const KvForm &f, int64_t tokens, const int64_t *slots, const void *cache, void *K,
                       void *V, cudaStream_t stream) {
-  return launch(dev, items, stream, kv_read_kernel<NB, T>, f, items, static_cast<T *>(K), static_cast<T *>(V), slots,
-                static_cast<uint8_t *>(const_cast<void *>(cache)));
+  return launch<NB>(dev, f, tokens, stream, kv_read_kernel<NB, T>, f, tokens, static_cast<T *>(K), static_cast<T *>(V), slots,
+                    static_cast<const uint8_t *>(cache));
 }
 
 // call<NB, element type>(...) for a cache's head size.
@@ -249,14 +353,12 @@ qmm_status launch_kv_write(const DevInfo &dev, const KvForm &f, int dtype, int64
                            int64_t ksh, const void *V, int64_t vst, int64_t vsh, const int64_t *slots, void *cache,
                            cudaStream_t stream) {
   const KvRows ks{kst, ksh}, vs{vst, vsh};
-  const int64_t items = T * f.heads * f.nb * 4;
-  return cuda_check(QMM_KV_FORM(write_rows, dev, f, items, K, ks, V, vs, slots, cache, stream), "kv_write launch");
+  return cuda_check(QMM_KV_FORM(write_rows, dev, f, T, K, ks, V, vs, slots, cache, stream), "kv_write launch");
 }
 
 qmm_status launch_kv_read(const DevInfo &dev, const KvForm &f, int dtype, int64_t T, const int64_t *slots,
                           const void *cache, void *K, void *V, cudaStream_t stream) {
-  const int64_t items = T * f.heads * f.nb * 4;
-  return cuda_check(QMM_KV_FORM(read_rows, dev, f, items, slots, cache, K, V, stream), "kv_read launch");
+  return cuda_check(QMM_KV_FORM(read_rows, dev, f, T, slots, cache, K, V, stream), "kv_read launch");
 }
 
 cudaError_t kv_cache_status(uint32_t *bits) {
