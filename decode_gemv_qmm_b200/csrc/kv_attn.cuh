@@ -89,7 +89,7 @@ struct KvCfg {
   static constexpr int kRows = 8 * OCT;
   static constexpr int kMT = FINE ? OCT : (OCT + 1) / 2;  // 16-row tiles: eight rows in two terms, or sixteen
   static constexpr int kQBytes = kMT * NB * 1024;         // a warp's query fragments
-  static constexpr int kBudget = 222 * 1024;
+  static constexpr int kBudget = 216 * 1024;  // of 227 KB; the rest is the static arrays
 #ifndef KV_TG1
 #define KV_TG1 4
 #endif
@@ -169,7 +169,7 @@ __device__ __forceinline__ int64_t kv_out_at(const KvLaunch &p, int s, int head,
 }
 
 // a * b / c without the slow 64-bit division where the numbers are small.
-__device__ __forceinline__ int64_t kv_muldiv(int64_t a, int64_t b, int64_t c) {
+static __device__ __noinline__ int64_t kv_muldiv(int64_t a, int64_t b, int64_t c) {
   const int64_t x = a * b;
   if ((static_cast<uint64_t>(x | c) >> 32) == 0) return static_cast<uint32_t>(x) / static_cast<uint32_t>(c);
   return x / c;
@@ -180,6 +180,22 @@ __device__ __forceinline__ int64_t kv_muldiv(int64_t a, int64_t b, int64_t c) {
 __device__ __forceinline__ int kv_block_of(int64_t at, int64_t blocks, int64_t total) {
   const int64_t x = (at + 1) * blocks - 1;
   return static_cast<int>(kv_muldiv(x, 1, total));
+}
+
+// Reads of partial results, in shared memory or in the scratch, where another
+// block may have written them.
+__device__ __forceinline__ float2 kv_load2(const float *p) {
+  float2 v;
+  asm volatile("ld.relaxed.gpu.v2.f32 {%0, %1}, [%2];" : "=f"(v.x), "=f"(v.y) : "l"(p) : "memory");
+  return v;
+}
+__device__ __forceinline__ float4 kv_load4(const float *p) {
+  float4 v;
+  asm volatile("ld.relaxed.gpu.v4.f32 {%0, %1, %2, %3}, [%4];"
+               : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+               : "l"(p)
+               : "memory");
+  return v;
 }
 
 // Four dims of a row, added up over partial results (maximum, sum; outputs), a
@@ -201,10 +217,6 @@ struct KvSum {
       l = fmaf(k, ml[i].y, l);
       o.x = fmaf(k, v[i].x, o.x), o.y = fmaf(k, v[i].y, o.y), o.z = fmaf(k, v[i].z, o.z), o.w = fmaf(k, v[i].w, o.w);
     }
-  }
-  __device__ __forceinline__ float4 result() const {
-    const float inv = l > 0.0f ? 1.0f / l : 0.0f;
-    return make_float4(o.x * inv, o.y * inv, o.z * inv, o.w * inv);
   }
 };
 
@@ -244,8 +256,12 @@ __device__ __forceinline__ void kv_attn_body(const KvLaunch &p, uint32_t *status
     int seq, head, tile, a, b, n;
     const float *out;
   };
+  struct Source {
+    const float *out, *ml;
+  };
   __shared__ Piece pieces[2 * NW];
   __shared__ float2 piece_ml[2 * NW][C::kRows];
+  __shared__ Source sources[kKvMaxBlocks];
   __shared__ int last_block;
 
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, t = lane & 3;
@@ -382,7 +398,6 @@ __device__ __forceinline__ void kv_attn_body(const KvLaunch &p, uint32_t *status
       use.head = item / p.tiles;
       use.tile = item - use.head * p.tiles;
       enter(use, pos - base - item * units);
-      if (use.a == use.b) next(use);
     }
   }
 
@@ -399,40 +414,40 @@ __device__ __forceinline__ void kv_attn_body(const KvLaunch &p, uint32_t *status
   const uint8_t *src = nullptr;
   int put_at = 0, put_n = 0, put_grp = put.first + put.a;
   uint32_t put_ok = 0;
-  auto window = [&]() {
-    const int grp = put_grp + lane, end = put.first + put.b;
-    put_n = min(end - put_grp, 32);
-    put_at = 0;
-    bool ok = false;
-    if (lane < put_n) {
-      const int page = __ldg(p.a.table + put.seq * p.a.table_stride + (grp >> page_shift));
-      ok = page >= 0 && page < p.f.pages;
-      if (!ok) atomicOr(status, kDevBadIndex);
-      src = p.a.cache + ((static_cast<int64_t>(page) * p.f.heads + put.head) * per_page + (grp & (per_page - 1))) *
-                            C::kGroupBytes;
-    }
-    put_ok = __ballot_sync(0xffffffffu, ok);
-  };
-  // Fill the ring's next stage with the next step of TG groups.
+  // Fill the ring's free stages, a step of TG groups each.
   auto fill = [&]() {
-    if (put_n == 0) return;
-    const int st = filled % S;
-    const uint32_t ok = put_ok >> put_at & ((1u << TG) - 1);
-    const int mine = lane - put_at;
-    if (mine == 0) mbar_arrive_expect_tx(bar + st, __popc(ok) * C::kGroupBytes);
-    __syncwarp();
-    if (mine >= 0 && mine < TG && (put_ok >> lane & 1))
-      bulk_g2s(ring + st * C::kStageBytes + mine * C::kGroupBytes, src, C::kGroupBytes, bar + st, policy);
-    ok_bits = (ok_bits & ~(((1u << TG) - 1) << (st * TG))) | ok << (st * TG);
-    ++filled;
-    put_at += TG;
-    if (put_at >= put_n) {
-      put_grp += put_n;
-      if (put_grp >= put.first + put.b) {
-        next(put);
-        put_grp = put.first + put.a;
+    while (filled - used < S) {
+      if (put_at >= put_n) {
+        put_grp += put_n;
+        put_n = put_at = 0;
+        if (put_grp >= put.first + put.b) {
+          if (put.left <= 0) return;
+          next(put);
+          put_grp = put.first + put.a;
+          if (put.a == put.b) return;
+        }
+        const int grp = put_grp + lane;
+        put_n = min(put.first + put.b - put_grp, 32);
+        bool ok = false;
+        if (lane < put_n) {
+          const int page = __ldg(p.a.table + put.seq * p.a.table_stride + (grp >> page_shift));
+          ok = page >= 0 && page < p.f.pages;
+          if (!ok) atomicOr(status, kDevBadIndex);
+          src = p.a.cache + ((static_cast<int64_t>(page) * p.f.heads + put.head) * per_page + (grp & (per_page - 1))) *
+                                C::kGroupBytes;
+        }
+        put_ok = __ballot_sync(0xffffffffu, ok);
       }
-      window();
+      const int st = filled % S;
+      const uint32_t ok = put_ok >> put_at & ((1u << TG) - 1);
+      const int mine = lane - put_at;
+      if (mine == 0) mbar_arrive_expect_tx(bar + st, __popc(ok) * C::kGroupBytes);
+      __syncwarp();
+      if (mine >= 0 && mine < TG && (put_ok >> lane & 1))
+        bulk_g2s(ring + st * C::kStageBytes + mine * C::kGroupBytes, src, C::kGroupBytes, bar + st, policy);
+      ok_bits = (ok_bits & ~(((1u << TG) - 1) << (st * TG))) | ok << (st * TG);
+      ++filled;
+      put_at += TG;
     }
   };
 
@@ -465,15 +480,15 @@ __device__ __forceinline__ void kv_attn_body(const KvLaunch &p, uint32_t *status
     }
   };
 
-  bool begun = false;
-  while (use.a < use.b) {
+  while (true) {
+    if (use.a == use.b) {
+      if (use.left <= 0) break;
+      next(use);
+      if (use.a == use.b) break;
+    }
     float4 rows[OCT][NB][2];
     load_rows(rows);
-    if (!begun) {  // the first copies while the rows are on their way
-      window();
-      for (int i = 0; i < S; ++i) fill();
-      begun = true;
-    }
+    if (!dead) fill();  // (the first item: nothing is on its way yet)
     float top[OCT], sum[OCT];  // of rows 8 o + g
     float2 acc[OCT][NB * 4];
     int last[OCT], low[OCT];
@@ -815,20 +830,18 @@ __device__ __forceinline__ void kv_attn_body(const KvLaunch &p, uint32_t *status
     const bool whole = use.a == 0 && use.b == use.n;
     const float down = __uint_as_float(static_cast<uint32_t>(127 - up_exp) << 23);
     const int piece = 2 * warp + (use.a == 0 ? 1 : 0);
-    const Place done = use;
-    next(use);
-    float *kept = use.a == use.b ? reinterpret_cast<float *>(own) : warp_slots + piece * C::kRows * D;
-    if (!whole && lane == 0) pieces[piece] = Piece{done.seq, done.head, done.tile, done.a, done.b, done.n, kept};
+    float *kept = use.left <= 0 ? reinterpret_cast<float *>(own) : warp_slots + piece * C::kRows * D;
+    if (!whole && lane == 0) pieces[piece] = Piece{use.seq, use.head, use.tile, use.a, use.b, use.n, kept};
     __syncwarp();
 #pragma unroll
     for (int o = 0; o < OCT; ++o) {
       float l = sum[o] * 0x1p-13f;
       l += __shfl_xor_sync(0xffffffffu, l, 1);
       l += __shfl_xor_sync(0xffffffffu, l, 2);
-      const int row = done.tile * C::kRows + o * 8 + g;
+      const int row = use.tile * C::kRows + o * 8 + g;
       if (row >= p.rows) continue;
       const float by = whole ? (l > 0.0f ? down / l : 0.0f) : down;
-      const int64_t out = kv_out_at(p, done.seq, done.head, row, D);
+      const int64_t out = kv_out_at(p, use.seq, use.head, row, D);
       float *part = kept + (o * 8 + g) * D;
       if (!whole && t == 0) piece_ml[piece][o * 8 + g] = make_float2(top[o], l);
 #pragma unroll
@@ -844,50 +857,61 @@ __device__ __forceinline__ void kv_attn_body(const KvLaunch &p, uint32_t *status
             *reinterpret_cast<float4 *>(part + d) = v;
         }
     }
+    use.a = use.b;
   }
 
-  // ---- the block's partial results, in the line's order ----
+  // ---- the block's partial results ----
+  // In the line's order. A warp's piece that begins its item (odd) begins a group
+  // of pieces of one item, the others go on with the one before.
   __syncthreads();
-  for (int e = 0; e < 2 * NW;) {
+  const uint32_t valid = __ballot_sync(0xffffffffu, lane < 2 * NW && pieces[min(lane, 2 * NW - 1)].seq >= 0);
+  uint32_t begins = (valid & 0xaaaaaaaau) | (valid & (0u - valid));
+#pragma unroll 1
+  while (begins) {
+    const int e = __ffs(begins) - 1;
+    begins &= begins - 1;
+    const uint32_t mine = valid & (begins ? (begins & (0u - begins)) - 1 : ~0u) & ~((1u << e) - 1);
     const Piece first = pieces[e];
-    if (first.seq < 0) {
-      ++e;
-      continue;
-    }
-    int stop = e + 1, b = first.b;
-    while (stop < 2 * NW && (pieces[stop].seq < 0 || (pieces[stop].seq == first.seq && pieces[stop].head == first.head &&
-                                                      pieces[stop].tile == first.tile))) {
-      if (pieces[stop].seq >= 0) b = pieces[stop].b;
-      ++stop;
-    }
-    const bool whole = first.a == 0 && b == first.n;
-    float *slot = block_slots + (first.a == 0 ? kSlot : 0);
-    for (int i = tid; i < C::kRows * (D / 4); i += kThreads) {
-      const int r = i / (D / 4), d = (i - r * (D / 4)) * 4, row = first.tile * C::kRows + r;
-      if (row >= p.rows) continue;
-      KvSum x;
-      for (int k = e; k < stop; k += 4) {
-        float2 ml[4];
-        float4 v[4];
+    bool whole = first.a == 0 && pieces[31 - __clz(mine)].b == first.n;
+    int n = __popc(mine);
+    if (tid < 2 * NW && (mine >> tid & 1))
+      sources[__popc(mine & ((1u << tid) - 1))] = Source{pieces[tid].out, &piece_ml[tid][0].x};
+    __syncthreads();
+    // First the block's pieces; then, if they are not the whole item and this is
+    // the last of its blocks, the blocks' results.
+#pragma unroll 1
+    while (true) {
+      float *slot = block_slots + (first.a == 0 ? kSlot : 0);
+#pragma unroll 1
+      for (int i = tid; i < C::kRows * (D / 4); i += kThreads) {
+        const int r = i / (D / 4), d = (i - r * (D / 4)) * 4, row = first.tile * C::kRows + r;
+        if (row >= p.rows) break;
+        KvSum x;
+#pragma unroll 1
+        for (int k = 0; k < n; k += 4) {
+          float2 ml[4];
+          float4 v[4];
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          ml[j] = make_float2(-INFINITY, 0.0f);
-          v[j] = make_float4(0.f, 0.f, 0.f, 0.f);
-          if (k + j < stop && pieces[min(k + j, 2 * NW - 1)].seq >= 0) {
-            ml[j] = piece_ml[k + j][r];
-            v[j] = *reinterpret_cast<const float4 *>(pieces[k + j].out + r * D + d);
+          for (int j = 0; j < 4; ++j) {
+            const Source s = sources[min(k + j, n - 1)];
+            ml[j] = kv_load2(s.ml + r * 2);
+            v[j] = kv_load4(s.out + r * D + d);
           }
+#pragma unroll
+          for (int j = 1; j < 4; ++j)
+            if (k + j >= n) ml[j].x = -INFINITY;
+          x.add(ml, v);
         }
-        x.add(ml, v);
+        if (whole) {
+          const float inv = x.l > 0.0f ? 1.0f / x.l : 0.0f;
+          kv_store(p, kv_out_at(p, first.seq, first.head, row, D) + d,
+                   make_float4(x.o.x * inv, x.o.y * inv, x.o.z * inv, x.o.w * inv));
+        } else {
+          *reinterpret_cast<float4 *>(slot + r * D + d) = x.o;
+          if (d == 0) *reinterpret_cast<float2 *>(slot + C::kRows * D + r * 2) = make_float2(x.m, x.l);
+        }
       }
-      if (whole) {
-        kv_store(p, kv_out_at(p, first.seq, first.head, row, D) + d, x.result());
-      } else {
-        *reinterpret_cast<float4 *>(slot + r * D + d) = x.o;
-        if (d == 0) *reinterpret_cast<float2 *>(slot + C::kRows * D + r * 2) = make_float2(x.m, x.l);
-      }
-    }
-    if (!whole) {
+      if (whole) break;
       // The item's blocks: those of its first group and of its last unit.
       int64_t at = scan[first.seq / chunk];
       for (int s = first.seq / chunk * chunk; s < first.seq; ++s) at += kv_units(kv_seq(p, s, status).n) * per_seq;
@@ -908,33 +932,16 @@ __device__ __forceinline__ void kv_attn_body(const KvLaunch &p, uint32_t *status
         if (last_block) *reinterpret_cast<volatile unsigned long long *>(counter) = p.epoch << 16;  // for a replay
         __threadfence();
       }
-      __syncthreads();
-      if (last_block) {
-        const float *parts = p.a.ws + kKvMaxBlocks * 4;
-        for (int i = tid; i < C::kRows * (D / 4); i += kThreads) {
-          const int r = i / (D / 4), d = (i - r * (D / 4)) * 4, row = first.tile * C::kRows + r;
-          if (row >= p.rows) continue;
-          KvSum x;
-          for (int k = b0; k <= b1; k += 8) {  // slot 1 of the first block, slot 0 of the others
-            float2 ml[8];
-            float4 v[8];
-#pragma unroll
-            for (int j = 0; j < 8; ++j) {
-              ml[j] = make_float2(-INFINITY, 0.0f);
-              v[j] = make_float4(0.f, 0.f, 0.f, 0.f);
-              if (k + j <= b1) {
-                const float *s = parts + (2 * (k + j) + (k + j == b0 ? 1 : 0)) * kSlot;
-                ml[j] = __ldcg(reinterpret_cast<const float2 *>(s + C::kRows * D + r * 2));
-                v[j] = __ldcg(reinterpret_cast<const float4 *>(s + r * D + d));
-              }
-            }
-            x.add(ml, v);
-          }
-          kv_store(p, kv_out_at(p, first.seq, first.head, row, D) + d, x.result());
-        }
+      n = b1 - b0 + 1;
+      for (int k = tid; k < n; k += kThreads) {  // slot 1 of the first block, slot 0 of the others
+        const float *s = p.a.ws + kKvMaxBlocks * 4 + (2 * (b0 + k) + (k == 0 ? 1 : 0)) * kSlot;
+        sources[k] = Source{s, s + C::kRows * D};
       }
+      __syncthreads();
+      if (!last_block) break;
+      whole = true;
     }
-    e = stop;
+    __syncthreads();  // the sources have been read
   }
 }
 
