@@ -38,6 +38,14 @@ __device__ __forceinline__ void split_f16(float2 x, __half2 &hi, __half2 &lo) {
   lo = __float22half2_rn(__ffma2_rn(__half22float2(hi), make_float2(-1.0f, -1.0f), x));
 }
 
+// Transposes an 8 x 8 tile of 16-bit values: lane (g, t) has row g, columns 2t and
+// 2t + 1, and gets column g, rows 2t and 2t + 1.
+__device__ __forceinline__ __half2 transpose8(__half2 x) {
+  uint32_t y;
+  asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(h2_bits(x)));
+  return bits_h2(y);
+}
+
 // Codes as fp16 pairs, exact: 0x6400 | c is 1024 + c. The constants come as
 // launch arguments: an instruction takes one immediate, and constants that the
 // compiler sees cost a second operation (measured: 64 of 487 instructions of 16
@@ -87,11 +95,14 @@ struct KvCfg {
   static constexpr int kKeyPart = kv_part_bytes(NB, KQ8);
   static constexpr int kGroupBytes = kKeyPart + kv_part_bytes(NB, VQ8);
   static constexpr int kRows = 8 * OCT;
-  static constexpr int kMT = FINE ? OCT : (OCT + 1) / 2;  // 16-row tiles: eight rows in two terms, or sixteen
-  static constexpr int kQBytes = kMT * NB * 1024;         // a warp's query fragments
+  static constexpr int kTerms = FINE ? 2 : 1;             // fp16 terms of a query or weight
+  static constexpr int kQBytes = OCT * NB * kTerms * 512;  // a warp's query fragments
   static constexpr int kBudget = 216 * 1024;  // of 227 KB; the rest is the static arrays
 #ifndef KV_TG1
 #define KV_TG1 4
+#endif
+#ifndef KV_TG2
+#define KV_TG2 2
 #endif
 #ifndef KV_TG4
 #define KV_TG4 1
@@ -102,7 +113,7 @@ struct KvCfg {
   static constexpr int warp_bytes(int tg, int stages) { return kQBytes + stages * tg * kGroupBytes; }
   static constexpr int kNW = KV_NW * warp_bytes(1, 2) <= kBudget ? KV_NW : KV_NW / 2;
   // groups of a step
-  static constexpr int kMaxTG = OCT == 1 ? KV_TG1 : OCT == 2 ? 2 : KV_TG4;
+  static constexpr int kMaxTG = OCT == 1 ? KV_TG1 : OCT == 2 ? KV_TG2 : KV_TG4;
   static constexpr bool fits(int tg) { return tg * kGroupBytes <= 9216 && kNW * warp_bytes(tg, 2) <= kBudget; }
   static constexpr int kTG = kMaxTG >= 4 && fits(4) ? 4 : kMaxTG >= 2 && fits(2) ? 2 : 1;
   static constexpr int stages() {
@@ -160,6 +171,13 @@ __device__ __forceinline__ void kv_store(const KvLaunch &p, int64_t at, float4 v
   } else {
     *reinterpret_cast<float4 *>(static_cast<float *>(p.a.out) + at) = v;
   }
+}
+
+__device__ __forceinline__ void kv_store(const KvLaunch &p, int64_t at, float2 v) {
+  if (p.bf16)
+    *reinterpret_cast<__nv_bfloat162 *>(static_cast<__nv_bfloat16 *>(p.a.out) + at) = __floats2bfloat162_rn(v.x, v.y);
+  else
+    *reinterpret_cast<float2 *>(static_cast<float *>(p.a.out) + at) = v;
 }
 
 // Output offset of row r (of one key/value head's M x ratio rows).
@@ -232,19 +250,21 @@ struct KvSum {
 // the item, or by the last of the item's blocks to be done (always in the
 // line's order: the same sums every time).
 //
-// Products run on the tensor cores with the cached codes as exact fp16
-// integers. fp32 queries (FINE): eight rows fill a 16-row tile, rows 0..7 with
-// the leading fp16 term and rows 8..15 with the remainder (22 bits together),
-// so fp32 accuracy costs no more products than the tile has. bf16 queries, and
-// the weights that go with them, are one term and fill sixteen rows. A key's
+// Products run on the tensor cores (mma.m16n8k16) with the cached codes, exact
+// fp16 integers, as the 16-row operand and an octet of query rows as the 8
+// columns: scores are keys x rows, outputs dims x rows, so a conversion serves
+// every octet and no column is wasted on terms. fp32 queries (FINE) and the
+// weights that go with them are two fp16 terms (22 bits together), each a product
+// of its own into the same sums; bf16 queries and their weights are one. A key's
 // block scale multiplies the finished 32-dim dot in fp32; a value's block scale
 // goes into the weight, p d_v, in fp16 with the product's own remainder (FINE).
-// Each step's sums are added to fp32 registers outside the tensor core, which
-// does not round its sums to nearest.
+// The weights change sides between the two products by 8 x 8 transposes. Each
+// step's sums are added to fp32 registers outside the tensor core, which does not
+// round its sums to nearest.
 template <int NB, bool KQ8, bool VQ8, int OCT, bool FINE>
 __device__ __forceinline__ void kv_attn_body(const KvLaunch &p, uint32_t *status) {
   using C = KvCfg<NB, KQ8, VQ8, OCT, FINE>;
-  constexpr int NW = C::kNW, TG = C::kTG, S = C::kStages, D = C::kD, MT = C::kMT;
+  constexpr int NW = C::kNW, TG = C::kTG, S = C::kStages, D = C::kD, TERMS = C::kTerms;
   constexpr int kThreads = NW * 32;
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ __align__(8) uint64_t bars[NW * S];
@@ -267,7 +287,7 @@ __device__ __forceinline__ void kv_attn_body(const KvLaunch &p, uint32_t *status
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, t = lane & 3;
   const KvMagic magic = p.magic;
   uint8_t *own = smem + warp * C::warp_bytes(TG, S);
-  uint4 *qfrag = reinterpret_cast<uint4 *>(own);  // [MT][NB][2][32]
+  uint4 *qfrag = reinterpret_cast<uint4 *>(own);  // [OCT][NB][TERMS][32]
   uint8_t *ring = own + C::kQBytes;
   const uint32_t qfrag_s = smem_u32(qfrag) + lane * 16, ring_s = smem_u32(ring);
   uint64_t *bar = bars + warp * S;
@@ -489,10 +509,10 @@ __device__ __forceinline__ void kv_attn_body(const KvLaunch &p, uint32_t *status
     float4 rows[OCT][NB][2];
     load_rows(rows);
     if (!dead) fill();  // (the first item: nothing is on its way yet)
-    float top[OCT], sum[OCT];  // of rows 8 o + g
-    float2 acc[OCT][NB * 4];
-    int last[OCT], low[OCT];
-    float factor[OCT];
+    // of rows 8 o + 2t and 8 o + 2t + 1
+    float2 top[OCT], sum[OCT], factor[OCT];
+    int2 last[OCT], low[OCT];
+    float2 acc[OCT][NB * 4];  // dims 2g, 16 + 2g, 2g + 1, 17 + 2g of each block
 
     // ---- query rows as fragments ----
     // Each row is brought to [2^14, 2^15) by a power of two so that both terms
@@ -502,7 +522,6 @@ __device__ __forceinline__ void kv_attn_body(const KvLaunch &p, uint32_t *status
     __syncwarp();
 #pragma unroll
     for (int o = 0; o < OCT; ++o) {
-      const int i = min((use.tile * C::kRows + o * 8 + g) / p.ratio, p.a.m - 1);
       float big = 0.0f;
 #pragma unroll
       for (int b = 0; b < NB; ++b)
@@ -516,34 +535,33 @@ __device__ __forceinline__ void kv_attn_body(const KvLaunch &p, uint32_t *status
       // exponent of the largest, at least -100 (smaller rows keep fewer bits of scores that are 0 anyway)
       const int ex = max(static_cast<int>(__float_as_uint(big) >> 23) - 127, -100);
       float up = __uint_as_float(static_cast<uint32_t>(14 - ex + 127) << 23);
-      factor[o] = p.a.scale == 0.0f ? 1.0f
-                                    : fabsf(p.a.scale) * 1.44269504088896f *
-                                          __uint_as_float(static_cast<uint32_t>(ex - 14 + 127) << 23);
+      const float f = p.a.scale == 0.0f ? 1.0f
+                                        : fabsf(p.a.scale) * 1.44269504088896f *
+                                              __uint_as_float(static_cast<uint32_t>(ex - 14 + 127) << 23);
+      factor[o] = make_float2(__shfl_sync(0xffffffffu, f, 8 * t), __shfl_sync(0xffffffffu, f, 8 * t + 4));
       if (p.a.scale <= 0.0f) up = p.a.scale < 0.0f ? -up : 0.0f;
 #pragma unroll
-      for (int b = 0; b < NB; ++b)
+      for (int b = 0; b < NB; ++b) {
+        __half2 hi[4], lo[4];
 #pragma unroll
         for (int half = 0; half < 2; ++half) {
           const float4 v = rows[o][b][half];
           const float2 even = make_float2(v.x * up, v.z * up), odd = make_float2(v.y * up, v.w * up);
-          uint32_t *f = reinterpret_cast<uint32_t *>(qfrag + (((FINE ? o : o / 2) * NB + b) * 2 + half) * 32 + lane);
-          if (FINE) {
-            __half2 h0, l0, h1, l1;
-            split_f16(even, h0, l0);
-            split_f16(odd, h1, l1);
-            *reinterpret_cast<uint4 *>(f) = make_uint4(h2_bits(h0), h2_bits(l0), h2_bits(h1), h2_bits(l1));
-          } else {
-            f[o & 1] = h2_bits(__float22half2_rn(even));
-            f[2 + (o & 1)] = h2_bits(__float22half2_rn(odd));
-            if (OCT == 1) f[1] = f[3] = 0u;
-          }
+          split_f16(even, hi[2 * half], lo[2 * half]);
+          split_f16(odd, hi[2 * half + 1], lo[2 * half + 1]);
         }
-      top[o] = -INFINITY;
-      sum[o] = 0.0f;
+        uint4 *f = qfrag + (o * NB + b) * TERMS * 32 + lane;
+        f[0] = make_uint4(h2_bits(hi[0]), h2_bits(hi[1]), h2_bits(hi[2]), h2_bits(hi[3]));
+        if (FINE) f[32] = make_uint4(h2_bits(lo[0]), h2_bits(lo[1]), h2_bits(lo[2]), h2_bits(lo[3]));
+      }
+      top[o] = make_float2(-INFINITY, -INFINITY);
+      sum[o] = make_float2(0.0f, 0.0f);
 #pragma unroll
       for (int n = 0; n < NB * 4; ++n) acc[o][n] = make_float2(0.0f, 0.0f);
-      last[o] = use.len - p.a.m + i;
-      low[o] = p.a.window > 0 ? max(0, last[o] - p.a.window + 1) : 0;
+      const int row = use.tile * C::kRows + o * 8 + 2 * t, off = use.len - p.a.m;
+      last[o] = make_int2(off + min(row / p.ratio, p.a.m - 1), off + min((row + 1) / p.ratio, p.a.m - 1));
+      low[o] = p.a.window > 0 ? make_int2(max(0, last[o].x - p.a.window + 1), max(0, last[o].y - p.a.window + 1))
+                              : make_int2(0, 0);
     }
     __syncwarp();
     const int low_all = p.a.window > 0 ? max(0, use.len - p.a.m - p.a.window + 1) : 0;
@@ -658,39 +676,38 @@ __device__ __forceinline__ void kv_attn_body(const KvLaunch &p, uint32_t *status
 #pragma unroll
         for (int r = 0; r < n; ++r) {
           const int b = first + r;
-          uint4 qa[MT][2];
+          uint4 q[OCT][TERMS];
 #pragma unroll
-          for (int mt = 0; mt < MT; ++mt) {
-            qa[mt][0] = lds_u4(qfrag_s + (mt * NB + b) * 1024);
-            qa[mt][1] = lds_u4(qfrag_s + (mt * NB + b) * 1024 + 512);
-          }
+          for (int o = 0; o < OCT; ++o)
+#pragma unroll
+            for (int i = 0; i < TERMS; ++i) q[o][i] = lds_u4(qfrag_s + ((o * NB + b) * TERMS + i) * 512);
 #pragma unroll
           for (int gi = 0; gi < TG; ++gi) {
-            const uint2 ks = lds_u2(stage + gi * C::kGroupBytes + kv_code_bytes(NB, KQ8) + (t * NB + b) * 8);
+            // keys (g >> 1) + 4 (g & 1) and 8 more are rows g and g + 8
+            uint4 k0, k1;
+            uint32_t *a0 = &k0.x, *a1 = &k1.x;
 #pragma unroll
             for (int j = 0; j < 2; ++j) {
-              uint32_t k00, k01, k10, k11;
               if (KQ8) {
                 const uint32_t w0 = kw[gi][j][(2 * r) & 3] ^ 0x80808080u, w1 = kw[gi][j][(2 * r + 1) & 3] ^ 0x80808080u;
-                k00 = q8_pair<0x5250>(w0, magic), k01 = q8_pair<0x5351>(w0, magic);
-                k10 = q8_pair<0x5250>(w1, magic), k11 = q8_pair<0x5351>(w1, magic);
+                a0[j] = q8_pair<0x5250>(w0, magic), a0[j + 2] = q8_pair<0x5351>(w0, magic);
+                a1[j] = q8_pair<0x5250>(w1, magic), a1[j + 2] = q8_pair<0x5351>(w1, magic);
               } else {
                 const uint32_t w = kw[gi][j][r], w8 = w >> 8;
-                k00 = q4_low(w, magic), k01 = q4_low(w8, magic), k10 = q4_high(w, magic), k11 = q4_high(w8, magic);
+                a0[j] = q4_low(w, magic), a0[j + 2] = q4_low(w8, magic);
+                a1[j] = q4_high(w, magic), a1[j + 2] = q4_high(w8, magic);
               }
-              const float2 d = __half22float2(bits_h2(j ? ks.y : ks.x));
+            }
+            const uint2 ks = lds_u2(stage + gi * C::kGroupBytes + kv_code_bytes(NB, KQ8) + ((g >> 1) * NB + b) * 8);
+            const float2 d = __half22float2(bits_h2(__byte_perm(ks.x, ks.y, g & 1 ? 0x7632 : 0x5410)));
 #pragma unroll
-              for (int mt = 0; mt < MT; ++mt) {
-                const float4 c = mma_f16(qa[mt][1], k10, k11,
-                                         mma_f16(qa[mt][0], k00, k01, make_float4(0.f, 0.f, 0.f, 0.f)));
-                const float2 upper = make_float2(c.x, c.y), lower = make_float2(c.z, c.w);
-                if (FINE) {
-                  z[mt][gi][j] = __ffma2_rn(d, __fadd2_rn(upper, lower), z[mt][gi][j]);
-                } else {
-                  z[2 * mt][gi][j] = __ffma2_rn(d, upper, z[2 * mt][gi][j]);
-                  if (OCT > 1) z[min(2 * mt + 1, OCT - 1)][gi][j] = __ffma2_rn(d, lower, z[min(2 * mt + 1, OCT - 1)][gi][j]);
-                }
-              }
+            for (int o = 0; o < OCT; ++o) {
+              float4 c = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+              for (int i = TERMS - 1; i >= 0; --i)
+                c = mma_f16(k1, q[o][i].z, q[o][i].w, mma_f16(k0, q[o][i].x, q[o][i].y, c));
+              z[o][gi][0] = __ffma2_rn(make_float2(d.x, d.x), make_float2(c.x, c.y), z[o][gi][0]);
+              z[o][gi][1] = __ffma2_rn(make_float2(d.y, d.y), make_float2(c.z, c.w), z[o][gi][1]);
             }
           }
         }
@@ -701,47 +718,57 @@ __device__ __forceinline__ void kv_attn_body(const KvLaunch &p, uint32_t *status
 #pragma unroll
         for (int gi = 0; gi < TG; ++gi)
 #pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const int key = key0 + gi * kKvGroup + t + 4 * e;
+          for (int j = 0; j < 2; ++j) {
+            const int key = key0 + gi * kKvGroup + (g >> 1) + 4 * (g & 1) + 8 * j;
 #pragma unroll
-            for (int o = 0; o < OCT; ++o)
-              if (!(ok >> gi & 1) || key > last[o] || key < low[o])
-                (e & 1 ? z[o][gi][e >> 1].y : z[o][gi][e >> 1].x) = -INFINITY;
+            for (int o = 0; o < OCT; ++o) {
+              if (!(ok >> gi & 1) || key > last[o].x || key < low[o].x) z[o][gi][j].x = -INFINITY;
+              if (!(ok >> gi & 1) || key > last[o].y || key < low[o].y) z[o][gi][j].y = -INFINITY;
+            }
           }
       }
 
       // ---- running maximum and sum ----
-      float keep[OCT];
-      __half2 ph[OCT][TG][2], pl[FINE ? OCT : 1][TG][2];
+      float2 keep[OCT];
+      __half2 ph[OCT][TG][2], pl[FINE ? OCT : 1][TG][2];  // weights, transposed: row g, keys t and t + 4 (and 8 more)
       const float turn = __uint_as_float(static_cast<uint32_t>(e_new - up_exp + 127) << 23);
       up_exp = e_new;
 #pragma unroll
       for (int o = 0; o < OCT; ++o) {
-        float m = -INFINITY;
+        float2 m = make_float2(-INFINITY, -INFINITY);
 #pragma unroll
-        for (int gi = 0; gi < TG; ++gi)
-          m = fmaxf(m, fmaxf(fmaxf(z[o][gi][0].x, z[o][gi][0].y), fmaxf(z[o][gi][1].x, z[o][gi][1].y)));
-        m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 1));
-        m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 2));
-        m = fmaxf(m * factor[o], top[o]);
-        const float ref = m == -INFINITY ? 0.0f : m, from13 = 13.0f - ref;
-        const float k = exp2_approx(top[o] - ref);
+        for (int gi = 0; gi < TG; ++gi) {
+          m.x = fmaxf(m.x, fmaxf(z[o][gi][0].x, z[o][gi][1].x));
+          m.y = fmaxf(m.y, fmaxf(z[o][gi][0].y, z[o][gi][1].y));
+        }
+#pragma unroll
+        for (int by = 4; by < 32; by <<= 1) {
+          m.x = fmaxf(m.x, __shfl_xor_sync(0xffffffffu, m.x, by));
+          m.y = fmaxf(m.y, __shfl_xor_sync(0xffffffffu, m.y, by));
+        }
+        m = make_float2(fmaxf(m.x * factor[o].x, top[o].x), fmaxf(m.y * factor[o].y, top[o].y));
+        const float2 ref = make_float2(m.x == -INFINITY ? 0.0f : m.x, m.y == -INFINITY ? 0.0f : m.y);
+        const float2 from13 = make_float2(13.0f - ref.x, 13.0f - ref.y);
+        const float2 k = make_float2(exp2_approx(top[o].x - ref.x), exp2_approx(top[o].y - ref.y));
         top[o] = m;
         float2 add = make_float2(0.0f, 0.0f);
 #pragma unroll
         for (int gi = 0; gi < TG; ++gi)
 #pragma unroll
           for (int j = 0; j < 2; ++j) {
-            float2 w = __ffma2_rn(z[o][gi][j], make_float2(factor[o], factor[o]), make_float2(from13, from13));
+            float2 w = __ffma2_rn(z[o][gi][j], factor[o], from13);
             w = make_float2(exp2_approx(w.x), exp2_approx(w.y));
             add = __fadd2_rn(add, w);
-            if (FINE)
-              split_f16(w, ph[o][gi][j], pl[FINE ? o : 0][gi][j]);
-            else
-              ph[o][gi][j] = __float22half2_rn(w);
+            if (FINE) {
+              __half2 h, l;
+              split_f16(w, h, l);
+              ph[o][gi][j] = transpose8(h), pl[FINE ? o : 0][gi][j] = transpose8(l);
+            } else {
+              ph[o][gi][j] = transpose8(__float22half2_rn(w));
+            }
           }
-        sum[o] = fmaf(sum[o], k, add.x + add.y);
-        keep[o] = k * turn;
+        sum[o] = __ffma2_rn(sum[o], k, add);
+        keep[o] = make_float2(k.x * turn, k.y * turn);
       }
 
       // ---- outputs ----
@@ -785,38 +812,30 @@ __device__ __forceinline__ void kv_attn_body(const KvLaunch &p, uint32_t *status
               }
             }
 #pragma unroll
-          for (int mt = 0; mt < MT; ++mt) {
-            float4 c[4];
+          for (int o = 0; o < OCT; ++o) {
+            float4 c[2] = {make_float4(0.f, 0.f, 0.f, 0.f), make_float4(0.f, 0.f, 0.f, 0.f)};
+            uint32_t w[TG][TERMS][2];
 #pragma unroll
-            for (int n4 = 0; n4 < 4; ++n4) c[n4] = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-            for (int gi = 0; gi < TG; ++gi) {
-              uint4 w;
+            for (int gi = 0; gi < TG; ++gi)
 #pragma unroll
               for (int j = 0; j < 2; ++j) {
-                const __half2 d = bits_h2(vs[gi][b][j]);
-                uint32_t &upper = j ? w.z : w.x, &lower = j ? w.w : w.y;
-                if (FINE) {  // p d_v = hi + what hi leaves of ph d_v + pl d_v
-                  const __half2 hi = __hmul2(ph[mt][gi][j], d);
-                  upper = h2_bits(hi);
-                  lower = h2_bits(__hfma2(pl[FINE ? mt : 0][gi][j], d, __hfma2(ph[mt][gi][j], d, __hneg2(hi))));
-                } else {
-                  upper = h2_bits(__hmul2(ph[2 * mt % OCT][gi][j], d));
-                  lower = OCT == 1 ? 0u : h2_bits(__hmul2(ph[min(2 * mt + 1, OCT - 1)][gi][j], d));
-                }
+                const __half2 d = bits_h2(vs[gi][b][j]), hi = __hmul2(ph[o][gi][j], d);
+                w[gi][0][j] = h2_bits(hi);
+                if (FINE)  // p d_v = hi + what hi leaves of ph d_v + pl d_v
+                  w[gi][TERMS - 1][j] = h2_bits(__hfma2(pl[FINE ? o : 0][gi][j], d, __hfma2(ph[o][gi][j], d, __hneg2(hi))));
               }
 #pragma unroll
-              for (int n4 = 0; n4 < 4; ++n4) c[n4] = mma_f16(w, vb[gi][n4][0], vb[gi][n4][1], c[n4]);
-            }
+            for (int i = TERMS - 1; i >= 0; --i)
 #pragma unroll
-            for (int n4 = 0; n4 < 4; ++n4) {
-              const float2 upper = make_float2(c[n4].x, c[n4].y), lower = make_float2(c[n4].z, c[n4].w);
-              const int i = b * 4 + n4, o = FINE ? mt : 2 * mt;
-              acc[o][i] = __ffma2_rn(acc[o][i], make_float2(keep[o], keep[o]), FINE ? __fadd2_rn(upper, lower) : upper);
-              if (!FINE && OCT > 1) {
-                const int q = min(o + 1, OCT - 1);
-                acc[q][i] = __ffma2_rn(acc[q][i], make_float2(keep[q], keep[q]), lower);
-              }
+              for (int gi = 0; gi < TG; ++gi)
+#pragma unroll
+                for (int h = 0; h < 2; ++h)
+                  c[h] = mma_f16(make_uint4(vb[gi][2 * h][0], vb[gi][2 * h + 1][0], vb[gi][2 * h][1], vb[gi][2 * h + 1][1]),
+                                 w[gi][i][0], w[gi][i][1], c[h]);
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+              acc[o][b * 4 + 2 * h] = __ffma2_rn(acc[o][b * 4 + 2 * h], keep[o], make_float2(c[h].x, c[h].y));
+              acc[o][b * 4 + 2 * h + 1] = __ffma2_rn(acc[o][b * 4 + 2 * h + 1], keep[o], make_float2(c[h].z, c[h].w));
             }
           }
         }
@@ -835,27 +854,31 @@ __device__ __forceinline__ void kv_attn_body(const KvLaunch &p, uint32_t *status
     __syncwarp();
 #pragma unroll
     for (int o = 0; o < OCT; ++o) {
-      float l = sum[o] * 0x1p-13f;
-      l += __shfl_xor_sync(0xffffffffu, l, 1);
-      l += __shfl_xor_sync(0xffffffffu, l, 2);
-      const int row = use.tile * C::kRows + o * 8 + g;
-      if (row >= p.rows) continue;
-      const float by = whole ? (l > 0.0f ? down / l : 0.0f) : down;
-      const int64_t out = kv_out_at(p, use.seq, use.head, row, D);
-      float *part = kept + (o * 8 + g) * D;
-      if (!whole && t == 0) piece_ml[piece][o * 8 + g] = make_float2(top[o], l);
+      float2 l = make_float2(sum[o].x * 0x1p-13f, sum[o].y * 0x1p-13f);
 #pragma unroll
-      for (int b = 0; b < NB; ++b)
+      for (int by = 4; by < 32; by <<= 1) {
+        l.x += __shfl_xor_sync(0xffffffffu, l.x, by);
+        l.y += __shfl_xor_sync(0xffffffffu, l.y, by);
+      }
 #pragma unroll
-        for (int half = 0; half < 2; ++half) {
-          const float2 x = acc[o][b * 4 + half], y = acc[o][b * 4 + half + 2];
-          const float4 v = make_float4(x.x * by, y.x * by, x.y * by, y.y * by);
-          const int d = b * 32 + half * 16 + 4 * t;
+      for (int i = 0; i < 2; ++i) {
+        const int r = o * 8 + 2 * t + i, row = use.tile * C::kRows + r;
+        if (row >= p.rows) continue;
+        const float li = i ? l.y : l.x;
+        if (!whole && g == 0) piece_ml[piece][r] = make_float2(i ? top[o].y : top[o].x, li);
+        const float by = whole ? (li > 0.0f ? down / li : 0.0f) : down;
+        const int64_t out = kv_out_at(p, use.seq, use.head, row, D) + 2 * g;
+        float *part = kept + r * D + 2 * g;
+#pragma unroll
+        for (int n = 0; n < NB * 2; ++n) {  // half blocks
+          const float2 x = acc[o][n / 2 * 4 + n % 2], y = acc[o][n / 2 * 4 + n % 2 + 2];
+          const float2 v = make_float2((i ? x.y : x.x) * by, (i ? y.y : y.x) * by);
           if (whole)
-            kv_store(p, out + d, v);
+            kv_store(p, out + n * 16, v);
           else
-            *reinterpret_cast<float4 *>(part + d) = v;
+            *reinterpret_cast<float2 *>(part + n * 16) = v;
         }
+      }
     }
     use.a = use.b;
   }
@@ -971,7 +994,8 @@ cudaError_t kv_attn_launch(const DevInfo &dev, KvLaunch &p, uint32_t *status, cu
 // Octets of rows that a warp takes at a time: the fewest that hold the rows, as
 // many at most as leave their sums in registers.
 constexpr int kv_attn_octets(int nb, int rows, bool fine) {
-  return rows <= 8 ? 1 : rows <= 16 || fine || nb > 4 ? 2 : 4;
+  const int most = fine || nb > 4 ? 2 : 4, need = (rows + 7) / 8;
+  return need < most ? need : most;
 }
 
 template <int NB, bool KQ8, bool VQ8, bool FINE>
@@ -979,6 +1003,9 @@ cudaError_t kv_attn_rows(const DevInfo &dev, KvLaunch &p, uint32_t *status, cons
   switch (kv_attn_octets(NB, p.rows, FINE)) {
     case 1: return kv_attn_launch<NB, KQ8, VQ8, 1, FINE>(dev, p, status, cfg);
     case 2: return kv_attn_launch<NB, KQ8, VQ8, 2, FINE>(dev, p, status, cfg);
+    case 3:
+      if constexpr (NB <= 4 && !FINE) return kv_attn_launch<NB, KQ8, VQ8, 3, FINE>(dev, p, status, cfg);
+      return cudaErrorInvalidValue;
     default:
       if constexpr (NB <= 4 && !FINE) return kv_attn_launch<NB, KQ8, VQ8, 4, FINE>(dev, p, status, cfg);
       return cudaErrorInvalidValue;
