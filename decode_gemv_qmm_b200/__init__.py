@@ -9,8 +9,8 @@ there is no fallback of any kind.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
-import functools
 import os
 
 import torch
@@ -22,6 +22,8 @@ if not os.path.exists(LIB_PATH):
     raise ImportError(f"{LIB_PATH} is missing: build it with `python decode_gemv_qmm_b200/build.py`")
 
 lib = ctypes.CDLL(LIB_PATH)
+
+from . import _qmm_bind  # noqa: E402  (built with the library; it links to it)
 
 QMM_OK, QMM_ERR_NULL, QMM_ERR_SHAPE, QMM_ERR_BLOCK, QMM_ERR_ALIGN = 0, 1, 2, 3, 4
 QMM_ERR_DTYPE, QMM_ERR_DEVICE, QMM_ERR_CUDA, QMM_ERR_DEVICE_CHECK = 5, 6, 7, 8
@@ -320,137 +322,63 @@ def qmm_prefill_plan(wtype: int, M: int, N: int, K: int, *, block: int = BLOCK) 
 
 # ---- quantised key/value cache ---------------------------------------------
 #
-# These calls are short on the GPU, so the checks here are plain comparisons and
-# messages are only made for what is refused.
-
-_KV_DTYPES = {torch.float32: QMM_F32, torch.bfloat16: QMM_BF16}
+# Calls of a few microseconds: their tensors are checked and passed on by native
+# code (csrc/qmm_bind.cpp).
 
 
-def _kv_refuse(fn: str, what: str):
-    raise ValueError(f"{fn}: {what}")
-
-
-def _kv_cache(fn: str, cache: torch.Tensor, size: int) -> int:
-    """Pages of a cache tensor (uint8 [pages, page_bytes], contiguous), checked against its form."""
-    if cache.dtype is not torch.uint8 or cache.dim() != 2 or not cache.is_contiguous():
-        _kv_refuse(fn, "cache is not a contiguous uint8 tensor [pages, page_bytes]")
-    pages, held = cache.shape
-    if held != size:
-        _kv_refuse(fn, f"pages of {held} bytes, this form has {size}")
-    return pages
-
-
-def _kv_rows(fn: str, name: str, t: torch.Tensor, dims: int, dev):
-    """(element type, shape, strides of the leading dims) of a tensor of rows; the stride of a dim that is not stepped
-    over is arbitrary and taken as 0."""
-    dtype, shape, stride = _KV_DTYPES.get(t.dtype), t.shape, t.stride()
-    if dtype is None:
-        _kv_refuse(fn, f"{name} is {t.dtype}, not float32 or bfloat16")
-    if len(shape) != dims or (stride[-1] != 1 and shape[-1] != 1 and t.numel()):
-        _kv_refuse(fn, f"{name} is not a tensor of {dims} dims with contiguous rows")
-    if t.device != dev:
-        _kv_refuse(fn, f"{name} is on {t.device}, the cache on {dev}")
-    if 1 in shape or 0 in shape:
-        none = 0 in shape
-        stride = [0 if n == 1 or none else v for n, v in zip(shape, stride)]
-    return dtype, shape, stride
-
-
-def _kv_index(fn: str, name: str, t: torch.Tensor, dtype, n: int, dev):
-    if t.dtype is not dtype or t.device != dev or t.shape != (n,) or not t.is_contiguous():
-        _kv_refuse(fn, f"{name} is not a contiguous {dtype} tensor of {n} on {dev}")
-
-
-_raw_stream = torch._C._cuda_getCurrentRawStream  # the current stream of a device, as an integer
-
-
-def _kv_elsewhere(dev: torch.device, stream) -> bool:
-    """Whether a call has to switch its device or stream first."""
-    return dev.type == "cuda" and (stream is not None or dev.index != torch.cuda.current_device())
-
-
-def _kv_switch(fn: str, dev: torch.device, stream):
-    """Context in which the tensors' device and the call's stream are the current ones, so that what the call
-    allocates belongs to that stream."""
-    if stream is None:
-        return torch.cuda.device(dev)
+@contextlib.contextmanager
+def _kv_on(fn: str, cache: torch.Tensor, stream):
+    """The call's stream (a torch stream or a handle) as the current one of the cache's device, so that what the
+    call allocates belongs to it."""
+    if not cache.is_cuda:
+        yield
+        return
     if isinstance(stream, int):
-        stream = torch.cuda.ExternalStream(stream, device=dev) if stream else torch.cuda.default_stream(dev)
-    if stream.device != dev:
-        _kv_refuse(fn, f"the stream is on {stream.device}, the cache on {dev}")
-    return torch.cuda.stream(stream)
-
-
-def _kv_current(dev: torch.device) -> int:
-    return _raw_stream(dev.index) if dev.type == "cuda" else 0
-
-
-@functools.lru_cache(maxsize=None)
-def _kv_page_bytes(Hkv, D, page, ktype, vtype, block) -> int:
-    out = ctypes.c_int64(0)
-    _check(lib.qmm_kv_page_bytes(ktype, vtype, Hkv, D, block, page, ctypes.addressof(out)), "qmm_kv_page_bytes")
-    return out.value
+        stream = (torch.cuda.ExternalStream(stream, device=cache.device) if stream
+                  else torch.cuda.default_stream(cache.device))
+    if stream.device != cache.device:
+        raise ValueError(f"{fn}: the stream is on {stream.device}, the cache on {cache.device}")
+    with torch.cuda.stream(stream):
+        yield
 
 
 def qmm_kv_page_bytes(Hkv: int, D: int, *, page: int, ktype: int = QMM_Q4_0, vtype: int = QMM_Q4_0,
                       block: int = BLOCK) -> int:
     """Bytes of a page of a key/value cache of this form."""
-    return _kv_page_bytes(Hkv, D, page, ktype, vtype, block)
+    out = ctypes.c_int64(0)
+    _check(lib.qmm_kv_page_bytes(ktype, vtype, Hkv, D, block, page, ctypes.addressof(out)), "qmm_kv_page_bytes")
+    return out.value
 
 
 def qmm_kv_write(cache: torch.Tensor, K: torch.Tensor, V: torch.Tensor, slots: torch.Tensor, *, page: int,
                  ktype: int = QMM_Q4_0, vtype: int = QMM_Q4_0, block: int = BLOCK, stream=None) -> torch.Tensor:
     """Quantise K, V [T, Hkv, D] (fp32 or bf16, rows contiguous) into the cache's slots int64 [T] (negative: left
     out; the others have to differ). cache: uint8 [pages, qmm_kv_page_bytes(Hkv, D, ...)]."""
-    fn, dev = "qmm_kv_write", cache.device
-    if _kv_elsewhere(dev, stream):
-        with _kv_switch(fn, dev, stream):
+    if stream is not None:
+        with _kv_on("qmm_kv_write", cache, stream):
             return qmm_kv_write(cache, K, V, slots, page=page, ktype=ktype, vtype=vtype, block=block)
-    dtype, shape, ks = _kv_rows(fn, "K", K, 3, dev)
-    vtype_, vshape, vs = _kv_rows(fn, "V", V, 3, dev)
-    if vshape != shape or vtype_ != dtype:
-        _kv_refuse(fn, "V is not of K's shape and type")
-    T, Hkv, D = shape
-    _kv_index(fn, "slots", slots, torch.int64, T, dev)
-    pages = _kv_cache(fn, cache, _kv_page_bytes(Hkv, D, page, ktype, vtype, block))
-    st = lib.qmm_kv_write(ktype, vtype, dtype, T, Hkv, D, block, pages, page, K.data_ptr(), ks[0], ks[1], V.data_ptr(),
-                          vs[0], vs[1], slots.data_ptr(), cache.data_ptr(), _kv_current(dev))
-    if st:
-        _check(st, fn)
-    return cache
+    out = _qmm_bind.write(cache, K, V, slots, page, ktype, vtype, block)
+    if out.__class__ is int:
+        _check(out, "qmm_kv_write")
+    return out
 
 
 def qmm_kv_read(cache: torch.Tensor, slots: torch.Tensor, Hkv: int, D: int, K: torch.Tensor | None = None,
                 V: torch.Tensor | None = None, *, page: int, ktype: int = QMM_Q4_0, vtype: int = QMM_Q4_0,
                 dtype: torch.dtype = torch.float32, block: int = BLOCK, stream=None):
     """(K, V) [T, Hkv, D]: the values of the cached tokens at slots int64 [T] (rows of a negative slot are left as
-    they were). dtype: float32 or bfloat16, that of K and V where they are given."""
-    fn, dev = "qmm_kv_read", cache.device
-    if _kv_elsewhere(dev, stream):
-        with _kv_switch(fn, dev, stream):
+    they were). dtype: float32 or bfloat16, where K is not given."""
+    if stream is not None:
+        with _kv_on("qmm_kv_read", cache, stream):
             return qmm_kv_read(cache, slots, Hkv, D, K, V, page=page, ktype=ktype, vtype=vtype, dtype=dtype, block=block)
-    T = slots.numel()
-    _kv_index(fn, "slots", slots, torch.int64, T, dev)
-    pages = _kv_cache(fn, cache, _kv_page_bytes(Hkv, D, page, ktype, vtype, block))
-    shape = (T, Hkv, D)
-    if K is None or V is None:
-        if dtype not in _KV_DTYPES:
-            _kv_refuse(fn, f"dtype is {dtype}, not float32 or bfloat16")
-        K = torch.empty(shape, dtype=dtype, device=dev) if K is None else K
-        V = torch.empty_like(K) if V is None else V
-    for t in (K, V):
-        if t.shape != shape or not t.is_contiguous() or t.device != dev or t.dtype not in _KV_DTYPES:
-            _kv_refuse(fn, f"K or V is not a contiguous fp32 or bf16 tensor {shape} on {dev}")
-    if K.dtype is not V.dtype:
-        _kv_refuse(fn, "K and V differ in type")
-    st = lib.qmm_kv_read(ktype, vtype, _KV_DTYPES[K.dtype], T, Hkv, D, block, pages, page, slots.data_ptr(),
-                         cache.data_ptr(), K.data_ptr(), V.data_ptr(), _kv_current(dev))
-    if st:
-        _check(st, fn)
-    return K, V
+    if dtype is not torch.float32 and dtype is not torch.bfloat16:
+        raise ValueError(f"qmm_kv_read: dtype is {dtype}, not float32 or bfloat16")
+    out = _qmm_bind.read(cache, slots, Hkv, D, K, V, dtype is torch.bfloat16, page, ktype, vtype, block)
+    if out.__class__ is int:
+        _check(out, "qmm_kv_read")
+    return out
 
 
-@functools.lru_cache(maxsize=None)
 def qmm_kv_attn_workspace(B: int, M: int, Hq: int, Hkv: int, D: int) -> int:
     """Scratch bytes of qmm_kv_attn for these sizes."""
     out = ctypes.c_int64(0)
@@ -466,33 +394,11 @@ def qmm_kv_attn(Q: torch.Tensor, cache: torch.Tensor, table: torch.Tensor, lens:
     sequence, its last M tokens, over its lens int32 [B] cached tokens; table int32 [B, max_pages] names the pages.
     scale: D ** -0.5 by default; window: how many keys a query sees (0: all up to its own). ws: uint8 scratch of
     qmm_kv_attn_workspace(...) bytes, allocated by default; calls that may run at the same time need their own."""
-    fn, dev = "qmm_kv_attn", cache.device
-    if _kv_elsewhere(dev, stream):
-        with _kv_switch(fn, dev, stream):
+    if stream is not None:
+        with _kv_on("qmm_kv_attn", cache, stream):
             return qmm_kv_attn(Q, cache, table, lens, Hkv, Y, ws, page=page, ktype=ktype, vtype=vtype, scale=scale,
                                window=window, block=block)
-    dtype, shape, qs = _kv_rows(fn, "Q", Q, 4, dev)
-    B, M, Hq, D = shape
-    if table.dtype is not torch.int32 or table.device != dev or table.dim() != 2 or table.shape[0] != B:
-        _kv_refuse(fn, f"table is not an int32 tensor of {B} rows on {dev}")
-    held, ts = table.shape[1], table.stride()
-    if held > 1 and ts[1] != 1:
-        _kv_refuse(fn, "table's rows are not contiguous")
-    _kv_index(fn, "lens", lens, torch.int32, B, dev)
-    pages = _kv_cache(fn, cache, _kv_page_bytes(Hkv, D, page, ktype, vtype, block))
-    need = qmm_kv_attn_workspace(B, M, Hq, Hkv, D)
-    if Y is None:
-        Y = Q.new_empty(shape)
-    elif Y.shape != shape or Y.dtype is not Q.dtype or Y.device != dev or not Y.is_contiguous():
-        _kv_refuse(fn, "Y is not a contiguous tensor of Q's shape, type and device")
-    if ws is None:
-        ws = cache.new_empty(need)
-    elif ws.dtype is not torch.uint8 or ws.device != dev or not ws.is_contiguous():
-        _kv_refuse(fn, "ws is not a contiguous uint8 tensor on the cache's device")
-    st = lib.qmm_kv_attn(ktype, vtype, dtype, B, M, Hq, Hkv, D, block, pages, page, Q.data_ptr(), qs[0], qs[1], qs[2],
-                         cache.data_ptr(), table.data_ptr(), ts[0] if B > 1 and held else 0, held, lens.data_ptr(),
-                         D ** -0.5 if scale is None else scale, window, Y.data_ptr(), ws.data_ptr(), ws.numel(),
-                         _kv_current(dev))
-    if st:
-        _check(st, fn)
-    return Y
+    out = _qmm_bind.attn(Q, cache, table, lens, Hkv, Y, ws, page, ktype, vtype, scale, window, block)
+    if out.__class__ is int:
+        _check(out, "qmm_kv_attn")
+    return out

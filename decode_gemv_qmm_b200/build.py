@@ -4,7 +4,9 @@
 
 Each csrc/*.cu is compiled to an object under _build/ (in parallel, only when
 it or a header changed) and the objects are linked into
-decode_gemv_qmm_b200/libqmm.so with the CUDA runtime linked statically.
+decode_gemv_qmm_b200/libqmm.so with the CUDA runtime linked statically. The
+Python entry of the key/value cache calls (csrc/qmm_bind.cpp) becomes
+decode_gemv_qmm_b200/_qmm_bind.so, built with g++ against the installed torch.
 """
 from __future__ import annotations
 
@@ -15,12 +17,14 @@ import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libqmm.so")
+BIND = os.path.join(PKG, "_qmm_bind.so")
 INCLUDE = os.path.join(ROOT, "include")
 
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
@@ -58,6 +62,34 @@ def _compile(src: str, obj: str, extra, verbose: bool) -> str:
     return (r.stdout + r.stderr).strip()
 
 
+def _build_bind(force: bool, verbose: bool) -> None:
+    """_qmm_bind.so, when it, its header or the installed torch changed."""
+    import torch
+
+    src, mark = os.path.join(CSRC, "qmm_bind.cpp"), BIND + ".torch"
+    made_with = open(mark).read() if os.path.exists(mark) else ""
+    newest = max(os.path.getmtime(f) for f in (src, os.path.join(INCLUDE, "qmm.h")))
+    if not force and os.path.exists(BIND) and os.path.getmtime(BIND) >= newest and made_with == torch.__version__:
+        return
+    root = os.path.dirname(torch.__file__)
+    cuda = os.path.dirname(os.path.dirname(nvcc()))
+    tmp = BIND + f".tmp{os.getpid()}"
+    cmd = [shutil.which("g++") or "g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-fvisibility=hidden",
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", "-I" + os.path.join(root, "include"),
+           "-I" + os.path.join(root, "include", "torch", "csrc", "api", "include"),
+           "-I" + sysconfig.get_paths()["include"], "-I" + os.path.join(cuda, "include"), src, "-o", tmp,
+           "-L" + os.path.join(root, "lib"), "-ltorch_python", "-ltorch", "-ltorch_cpu", "-lc10", "-lc10_cuda",
+           "-L" + PKG, "-l:libqmm.so", "-Wl,-rpath,$ORIGIN"]
+    if verbose:
+        print(" ".join(cmd), flush=True)
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"g++ failed on {os.path.basename(src)}:\n{r.stdout}\n{r.stderr}")
+    os.replace(tmp, BIND)
+    with open(mark, "w") as f:
+        f.write(torch.__version__)
+
+
 def build(force: bool = False, verbose: bool = False, extra_flags=()) -> str:
     os.makedirs(BUILD, exist_ok=True)
     srcs = _sources()
@@ -83,6 +115,7 @@ def build(force: bool = False, verbose: bool = False, extra_flags=()) -> str:
             print(" ".join(cmd), flush=True)
         subprocess.run(cmd, check=True)
         os.replace(tmp, LIB)
+    _build_bind(force, verbose)
     return LIB
 
 
