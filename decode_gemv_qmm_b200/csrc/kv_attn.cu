@@ -18,12 +18,12 @@ qmm_status launch_kv_attn(const DevInfo &dev, const KvForm &f, int dtype, const 
   p.a = a;
   p.ratio = a.hq / f.heads;
   p.rows = a.m * p.ratio;
-  p.min_units = kKvItemCost + 2;
+  p.min_units = 4;
   p.bf16 = dtype == QMM_BF16;
-  // A number that no other call has, 48 bits of it; the start keeps processes apart.
+  // A number that no other call has; the start keeps it from what scratch memory may hold.
   static std::atomic<uint64_t> calls{static_cast<uint64_t>(std::chrono::steady_clock::now().time_since_epoch().count()) *
                                      0x9e3779b97f4a7c15ull};
-  p.epoch = calls.fetch_add(1, std::memory_order_relaxed) & 0xffffffffffffull;
+  p.epoch = calls.fetch_add(1, std::memory_order_relaxed) | 1ull << 63;
   p.magic = KvMagic{0x64006400u, 0x2c002c00u, 0xd480d480u};
   // The status word's address on this device, looked up once.
   static std::atomic<uint32_t *> words[64];

@@ -84,7 +84,7 @@ constexpr int kKvMaxWarps = 8;     // most warps of a block
 #endif
 constexpr int kKvItemCost = KV_ITEM_COST;  // what beginning an item costs, in groups
 
-// Scratch: a counter for each block, two partial results of each block, two of each warp.
+// Scratch: two marks and two partial results of each block, two outputs of each warp.
 __host__ __device__ constexpr int64_t kv_attn_scratch_floats(int rows, int d) {
   return kKvMaxBlocks * (4 + 2 * kv_attn_slot_floats(rows, d) + 2 * kKvMaxWarps * rows * d);
 }
@@ -137,7 +137,7 @@ struct KvLaunch {
   int min_units;           // least units of the line for a warp
   int bf16;
   KvMagic magic;
-  uint64_t epoch;          // marks this call's counters
+  uint64_t epoch;          // this call's mark, not 0
 };
 
 // Groups of 16 tokens that the queries of sequence s see: [first, first + n).
@@ -186,19 +186,22 @@ __device__ __forceinline__ int64_t kv_out_at(const KvLaunch &p, int s, int head,
   return ((static_cast<int64_t>(s) * p.a.m + i) * p.a.hq + head * p.ratio + h) * d;
 }
 
-// a * b / c without the slow 64-bit division where the numbers are small.
-static __device__ __noinline__ int64_t kv_muldiv(int64_t a, int64_t b, int64_t c) {
-  const int64_t x = a * b;
-  if ((static_cast<uint64_t>(x | c) >> 32) == 0) return static_cast<uint32_t>(x) / static_cast<uint32_t>(c);
-  return x / c;
+// a / b of numbers >= 0, without the slow 64-bit division where they are small.
+static __device__ __noinline__ int64_t kv_div(int64_t a, int64_t b) {
+  if ((static_cast<uint64_t>(a | b) >> 32) == 0) return static_cast<uint32_t>(a) / static_cast<uint32_t>(b);
+  return a / b;
 }
 
-// The block that has place `at` of the line, block i's run being [i total / blocks,
-// (i + 1) total / blocks).
-__device__ __forceinline__ int kv_block_of(int64_t at, int64_t blocks, int64_t total) {
-  const int64_t x = (at + 1) * blocks - 1;
-  return static_cast<int>(kv_muldiv(x, 1, total));
-}
+// A line of `total` units over `blocks`: the first `more` have one more than `each`.
+struct KvShare {
+  int64_t each, more;
+  __device__ __forceinline__ int64_t begin(int i) const { return i * each + min(static_cast<int64_t>(i), more); }
+  // the block that has place `at`
+  __device__ __forceinline__ int block_of(int64_t at) const {
+    const int64_t wide = more * (each + 1);
+    return static_cast<int>(at < wide ? kv_div(at, each + 1) : more + kv_div(at - wide, each));
+  }
+};
 
 // Reads of partial results, in shared memory or in the scratch, where another
 // block may have written them.
@@ -276,13 +279,22 @@ __device__ __forceinline__ void kv_attn_body(const KvLaunch &p, uint32_t *status
     int seq, head, tile, a, b, n;
     const float *out;
   };
-  struct Source {
-    const float *out, *ml;
+  // A warp's place on the line: an item's groups [a, b) of n, and the units behind them.
+  struct Place {
+    int seq, head, tile, len, first, n, a, b;
+    int64_t left;
+  };
+  __shared__ Place puts[NW];  // where the copies are
+  struct Job {  // what is added up: an item's pieces (as bits), or its blocks' results from a first block on
+    int seq, head, tile, a;
+    uint32_t pieces;
+    int n;
+    bool whole;
   };
   __shared__ Piece pieces[2 * NW];
   __shared__ float2 piece_ml[2 * NW][C::kRows];
-  __shared__ Source sources[kKvMaxBlocks];
-  __shared__ int last_block;
+  __shared__ Job jobs[2 * NW], joins[2];
+  __shared__ KvShare kept_share;
 
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, t = lane & 3;
   const KvMagic magic = p.magic;
@@ -347,19 +359,19 @@ __device__ __forceinline__ void kv_attn_body(const KvLaunch &p, uint32_t *status
 
   // Blocks that work, this block's run of the line, and this warp's part of it.
   const int64_t least = static_cast<int64_t>(p.min_units) * NW;
-  const int64_t blocks = min(static_cast<int64_t>(gridDim.x), kv_muldiv(total + least - 1, 1, least));
-  unsigned long long *counters = reinterpret_cast<unsigned long long *>(p.a.ws);
+  int blocks = gridDim.x;
+  if (total < blocks * least) blocks = static_cast<int>(kv_div(total + least - 1, least));
+  volatile uint64_t *marks = reinterpret_cast<volatile uint64_t *>(p.a.ws);  // two of each block
   constexpr int64_t kSlot = kv_attn_slot_floats(C::kRows, D);
   float *block_slots = p.a.ws + kKvMaxBlocks * 4 + 2 * blockIdx.x * kSlot;
   float *warp_slots = p.a.ws + kKvMaxBlocks * (4 + 2 * kSlot) + 2 * NW * blockIdx.x * C::kRows * D;
   if (blockIdx.x >= blocks) return;
-  const int64_t from = kv_muldiv(blockIdx.x, total, blocks), span = kv_muldiv(blockIdx.x + 1, total, blocks) - from;
+  KvShare share;
+  share.each = kv_div(total, blocks);
+  share.more = total - share.each * blocks;
+  if (tid == 0) kept_share = share;  // (for the end: not in registers over the work)
+  const int64_t from = share.begin(blockIdx.x), span = share.begin(blockIdx.x + 1) - from;
 
-  // A warp's place on the line: an item's groups [a, b) of n, and the units behind them.
-  struct Place {
-    int seq, head, tile, len, first, n, a, b;
-    int64_t left;
-  };
   // The part of the item at hand that begins `skip` units into it.
   auto enter = [&](Place &c, int64_t skip) {
     const int64_t a = max(skip - kKvItemCost, int64_t(0));
@@ -397,16 +409,22 @@ __device__ __forceinline__ void kv_attn_body(const KvLaunch &p, uint32_t *status
     const int64_t pos = from + span * warp / NW;  // (NW is a power of two)
     use.left = from + span * (warp + 1) / NW - pos;
     if (use.left > 0) {
-      int lo = 0, hi = kThreads;  // scan[lo] <= pos < scan[hi]
-      while (hi - lo > 1) {
-        const int mid = (lo + hi) >> 1;
-        if (scan[mid] <= pos)
-          lo = mid;
-        else
-          hi = mid;
+      int64_t base;
+      if (p.a.batch <= 32) {
+        use.seq = __popc(__ballot_sync(0xffffffffu, scan[lane + 1] <= pos));
+        base = scan[use.seq];
+      } else {
+        int lo = 0, hi = kThreads;  // scan[lo] <= pos < scan[hi]
+        while (hi - lo > 1) {
+          const int mid = (lo + hi) >> 1;
+          if (scan[mid] <= pos)
+            lo = mid;
+          else
+            hi = mid;
+        }
+        base = scan[lo];
+        use.seq = lo * chunk;
       }
-      int64_t base = scan[lo];
-      use.seq = lo * chunk;
       look(use);
       while (pos >= base + kv_units(use.n) * per_seq) {
         base += kv_units(use.n) * per_seq;
@@ -414,7 +432,7 @@ __device__ __forceinline__ void kv_attn_body(const KvLaunch &p, uint32_t *status
         look(use);
       }
       const int64_t units = kv_units(use.n);
-      const int item = static_cast<int>(kv_muldiv(pos - base, 1, units));
+      const int item = static_cast<int>(kv_div(pos - base, units));
       use.head = item / p.tiles;
       use.tile = item - use.head * p.tiles;
       enter(use, pos - base - item * units);
@@ -423,7 +441,8 @@ __device__ __forceinline__ void kv_attn_body(const KvLaunch &p, uint32_t *status
 
   const int per_page = p.f.page / kKvGroup, page_shift = 31 - __clz(per_page);
   const uint64_t policy = l2_evict_first_policy();
-  Place put = use;
+  if (lane == 0) puts[warp] = use;
+  __syncwarp();
   uint32_t filled = 0, used = 0;  // stages of the ring so far
   uint32_t ok_bits = 0;           // groups in the ring whose page exists
   bool dead = false;              // a wait ran out
@@ -432,7 +451,7 @@ __device__ __forceinline__ void kv_attn_body(const KvLaunch &p, uint32_t *status
   // address of one of the next 32 groups of the item at hand (put_at counts
   // those copied, put_n those there are, put_ok marks the ones whose page exists).
   const uint8_t *src = nullptr;
-  int put_at = 0, put_n = 0, put_grp = put.first + put.a;
+  int put_at = 0, put_n = 0, put_grp = use.first + use.a, put_end = use.first + use.b;
   uint32_t put_ok = 0;
   // Fill the ring's free stages, a step of TG groups each.
   auto fill = [&]() {
@@ -440,14 +459,19 @@ __device__ __forceinline__ void kv_attn_body(const KvLaunch &p, uint32_t *status
       if (put_at >= put_n) {
         put_grp += put_n;
         put_n = put_at = 0;
-        if (put_grp >= put.first + put.b) {
+        Place put = puts[warp];
+        if (put_grp >= put_end) {
           if (put.left <= 0) return;
           next(put);
+          __syncwarp();
+          if (lane == 0) puts[warp] = put;
+          __syncwarp();
           put_grp = put.first + put.a;
-          if (put.a == put.b) return;
+          put_end = put.first + put.b;
+          if (put_grp >= put_end) return;
         }
         const int grp = put_grp + lane;
-        put_n = min(put.first + put.b - put_grp, 32);
+        put_n = min(put_end - put_grp, 32);
         bool ok = false;
         if (lane < put_n) {
           const int page = __ldg(p.a.table + put.seq * p.a.table_stride + (grp >> page_shift));
@@ -883,88 +907,104 @@ __device__ __forceinline__ void kv_attn_body(const KvLaunch &p, uint32_t *status
     use.a = use.b;
   }
 
-  // ---- the block's partial results ----
-  // In the line's order. A warp's piece that begins its item (odd) begins a group
-  // of pieces of one item, the others go on with the one before.
+  // ---- partial results ----
+  // In the line's order a warp's piece that begins its item (odd) begins a group
+  // of pieces of one item, the others go on with the one before. A group is
+  // added up by warps, 32 quads of outputs each, to the result if it is the whole
+  // item, else to one of the block's two slots (only its first and its last item
+  // can lie in other blocks too). Then those two, if this block is the last of
+  // theirs to be done, from all their blocks' slots.
   __syncthreads();
   const uint32_t valid = __ballot_sync(0xffffffffu, lane < 2 * NW && pieces[min(lane, 2 * NW - 1)].seq >= 0);
-  uint32_t begins = (valid & 0xaaaaaaaau) | (valid & (0u - valid));
-#pragma unroll 1
-  while (begins) {
-    const int e = __ffs(begins) - 1;
-    begins &= begins - 1;
-    const uint32_t mine = valid & (begins ? (begins & (0u - begins)) - 1 : ~0u) & ~((1u << e) - 1);
+  const uint32_t begins = (valid & 0xaaaaaaaau) | (valid & (0u - valid));
+  const int groups = __popc(begins);
+  constexpr int kChunks = (C::kRows * (D / 4) + 31) / 32;
+  if (tid < groups) {
+    const int e = __fns(begins, 0, tid + 1);
+    const uint32_t after = begins & ~((2u << e) - 1), mine = valid & (after ? (after & (0u - after)) - 1 : ~0u) & ~((1u << e) - 1);
     const Piece first = pieces[e];
-    bool whole = first.a == 0 && pieces[31 - __clz(mine)].b == first.n;
-    int n = __popc(mine);
-    if (tid < 2 * NW && (mine >> tid & 1))
-      sources[__popc(mine & ((1u << tid) - 1))] = Source{pieces[tid].out, &piece_ml[tid][0].x};
-    __syncthreads();
-    // First the block's pieces; then, if they are not the whole item and this is
-    // the last of its blocks, the blocks' results.
+    jobs[tid] = Job{first.seq, first.head, first.tile, first.a, mine, __popc(mine),
+                    first.a == 0 && pieces[31 - __clz(mine)].b == first.n};
+  }
+  __syncthreads();
+  if (groups == 0) return;
+  int njobs = groups;
 #pragma unroll 1
-    while (true) {
-      float *slot = block_slots + (first.a == 0 ? kSlot : 0);
+  for (int phase = 0; phase < 2; ++phase) {
 #pragma unroll 1
-      for (int i = tid; i < C::kRows * (D / 4); i += kThreads) {
-        const int r = i / (D / 4), d = (i - r * (D / 4)) * 4, row = first.tile * C::kRows + r;
-        if (row >= p.rows) break;
-        KvSum x;
+    for (int it = warp; it < njobs * kChunks; it += NW) {
+      const int job = it / kChunks, i = (it - job * kChunks) * 32 + lane, r = i / (D / 4), d = (i - r * (D / 4)) * 4;
+      const Job w = jobs[job];
+      const int row = w.tile * C::kRows + r;
+      if (r >= C::kRows || row >= p.rows) continue;
+      KvSum x;
+      uint32_t left = w.pieces;  // phase 0: the group's pieces; phase 1: its first block
 #pragma unroll 1
-        for (int k = 0; k < n; k += 4) {
-          float2 ml[4];
-          float4 v[4];
+      for (int k = 0; k < w.n; k += 8) {
+        float2 ml[8];
+        float4 v[8];
 #pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            const Source s = sources[min(k + j, n - 1)];
-            ml[j] = kv_load2(s.ml + r * 2);
-            v[j] = kv_load4(s.out + r * D + d);
+        for (int j = 0; j < 8; ++j) {
+          const float *o, *m;
+          if (phase == 0) {
+            const int e = __ffs(left) - 1;
+            if (left & (left - 1)) left &= left - 1;
+            o = pieces[e].out, m = &piece_ml[e][0].x;
+          } else {  // slot 1 of the first block, slot 0 of the others
+            const int part = min(k + j, w.n - 1);
+            o = p.a.ws + kKvMaxBlocks * 4 + (2 * (static_cast<int>(w.pieces) + part) + (part == 0 ? 1 : 0)) * kSlot;
+            m = o + C::kRows * D;
           }
-#pragma unroll
-          for (int j = 1; j < 4; ++j)
-            if (k + j >= n) ml[j].x = -INFINITY;
-          x.add(ml, v);
+          ml[j] = kv_load2(m + r * 2);
+          v[j] = kv_load4(o + r * D + d);
+          if (k + j >= w.n) ml[j].x = -INFINITY;
         }
-        if (whole) {
-          const float inv = x.l > 0.0f ? 1.0f / x.l : 0.0f;
-          kv_store(p, kv_out_at(p, first.seq, first.head, row, D) + d,
-                   make_float4(x.o.x * inv, x.o.y * inv, x.o.z * inv, x.o.w * inv));
-        } else {
-          *reinterpret_cast<float4 *>(slot + r * D + d) = x.o;
-          if (d == 0) *reinterpret_cast<float2 *>(slot + C::kRows * D + r * 2) = make_float2(x.m, x.l);
-        }
+        x.add(ml, v);
       }
-      if (whole) break;
-      // The item's blocks: those of its first group and of its last unit.
-      int64_t at = scan[first.seq / chunk];
-      for (int s = first.seq / chunk * chunk; s < first.seq; ++s) at += kv_units(kv_seq(p, s, status).n) * per_seq;
-      at += (static_cast<int64_t>(first.head) * p.tiles + first.tile) * kv_units(first.n);
-      const int b0 = kv_block_of(at + kKvItemCost, blocks, total);
-      const int b1 = kv_block_of(at + kv_units(first.n) - 1, blocks, total);
-      __threadfence();
-      __syncthreads();
-      if (tid == 0) {
-        // Counters need no first value: one that another call left has another epoch.
-        unsigned long long *counter = counters + b0, seen = *reinterpret_cast<volatile unsigned long long *>(counter), now;
-        do {
-          now = seen;
-          const unsigned long long count = (now >> 16) == p.epoch ? now : p.epoch << 16;
-          seen = atomicCAS(counter, now, count + 1);
-          last_block = static_cast<int>(count & 0xffff) == b1 - b0;
-        } while (seen != now);
-        if (last_block) *reinterpret_cast<volatile unsigned long long *>(counter) = p.epoch << 16;  // for a replay
-        __threadfence();
+      if (w.whole) {
+        const float inv = x.l > 0.0f ? 1.0f / x.l : 0.0f;
+        kv_store(p, kv_out_at(p, w.seq, w.head, row, D) + d,
+                 make_float4(x.o.x * inv, x.o.y * inv, x.o.z * inv, x.o.w * inv));
+      } else {
+        float *slot = block_slots + (w.a == 0 ? kSlot : 0);
+        *reinterpret_cast<float4 *>(slot + r * D + d) = x.o;
+        if (d == 0) *reinterpret_cast<float2 *>(slot + C::kRows * D + r * 2) = make_float2(x.m, x.l);
       }
-      n = b1 - b0 + 1;
-      for (int k = tid; k < n; k += kThreads) {  // slot 1 of the first block, slot 0 of the others
-        const float *s = p.a.ws + kKvMaxBlocks * 4 + (2 * (b0 + k) + (k == 0 ? 1 : 0)) * kSlot;
-        sources[k] = Source{s, s + C::kRows * D};
-      }
-      __syncthreads();
-      if (!last_block) break;
-      whole = true;
     }
-    __syncthreads();  // the sources have been read
+    if (phase) break;
+    const int split0 = !jobs[0].whole, split1 = groups > 1 && !jobs[groups - 1].whole;
+    if (!split0 && !split1) break;
+    __syncthreads();
+    if (warp < 2 && (warp ? split1 : split0)) {
+      const Job w = jobs[warp ? groups - 1 : 0];
+      const KvShare share = kept_share;
+      // The item's blocks: those of its first group and of its last unit.
+      int64_t at = scan[w.seq / chunk];
+      for (int s = w.seq / chunk * chunk; s < w.seq; ++s) at += kv_units(kv_seq(p, s, status).n) * per_seq;
+      const int64_t units = kv_units(kv_seq(p, w.seq, status).n);
+      at += (static_cast<int64_t>(w.head) * p.tiles + w.tile) * units;
+      const int b0 = share.block_of(at + kKvItemCost), n = share.block_of(at + units - 1) - b0 + 1;
+      // Marks need no first value: one that another call left is not this call's.
+      // Of two blocks that end at once each may find all marks and join: the
+      // results are the same. The joining block takes the marks off, for a replay.
+      const auto mark_of = [&](int k) { return marks + 2 * (b0 + k) + (k == 0 ? 1 : 0); };
+      __threadfence();  // (the block's results, written before the barrier)
+      if (lane == 0) *mark_of(blockIdx.x - b0) = p.epoch;
+      __syncwarp();
+      __threadfence();
+      bool all = true;
+      for (int k = lane; k < n; k += 32) all = all && *mark_of(k) == p.epoch;
+      all = __all_sync(0xffffffffu, all);
+      __threadfence();
+      if (all)
+        for (int k = lane; k < n; k += 32) *mark_of(k) = 0;
+      if (lane == 0) joins[warp] = Job{w.seq, w.head, w.tile, 0, static_cast<uint32_t>(b0), all ? n : 0, true};
+    }
+    __syncthreads();
+    const int join0 = split0 && joins[0].n, join1 = split1 && joins[1].n;
+    njobs = join0 + join1;
+    if (tid < njobs) jobs[tid] = joins[tid == 0 && join0 ? 0 : 1];
+    __syncthreads();
   }
 }
 
