@@ -679,8 +679,8 @@ __device__ __forceinline__ void kv_attn_body(const KvLaunch &p, uint32_t *status
 #pragma unroll
         for (int gi = 0; gi < TG; ++gi) z[o][gi][0] = z[o][gi][1] = make_float2(0.0f, 0.0f);
 #pragma unroll
-      for (int first = 0; first < NB;) {
-        const int n = kv_run(NB, KQ8, first).n, bytes = n * (KQ8 ? 8 : 4);
+      for (int run = 0; run < kv_runs(NB, KQ8); ++run) {
+        const int first = kv_run_first(NB, KQ8, run), n = kv_run_blocks(NB, KQ8, run), bytes = n * (KQ8 ? 8 : 4);
         uint32_t kw[TG][2][4];
 #pragma unroll
         for (int gi = 0; gi < TG; ++gi)
@@ -698,7 +698,8 @@ __device__ __forceinline__ void kv_attn_body(const KvLaunch &p, uint32_t *status
             }
           }
 #pragma unroll
-        for (int r = 0; r < n; ++r) {
+        for (int r = 0; r < (KQ8 ? 2 : 4); ++r) {
+          if (r >= n) continue;
           const int b = first + r;
           uint4 q[OCT][TERMS];
 #pragma unroll
@@ -735,7 +736,6 @@ __device__ __forceinline__ void kv_attn_body(const KvLaunch &p, uint32_t *status
             }
           }
         }
-        first += n;
       }
 
       if (!full) {
@@ -797,8 +797,8 @@ __device__ __forceinline__ void kv_attn_body(const KvLaunch &p, uint32_t *status
 
       // ---- outputs ----
 #pragma unroll
-      for (int first = 0; first < NB;) {
-        const int n = kv_run(NB, VQ8, first).n, wide = VQ8 ? 4 : 2, bytes = n * wide;
+      for (int run = 0; run < kv_runs(NB, VQ8); ++run) {
+        const int first = kv_run_first(NB, VQ8, run), n = kv_run_blocks(NB, VQ8, run), wide = VQ8 ? 4 : 2, bytes = n * wide;
         uint32_t vw[TG][4][2];
 #pragma unroll
         for (int gi = 0; gi < TG; ++gi)
@@ -815,7 +815,8 @@ __device__ __forceinline__ void kv_attn_body(const KvLaunch &p, uint32_t *status
             }
           }
 #pragma unroll
-        for (int r = 0; r < n; ++r) {
+        for (int r = 0; r < (VQ8 ? 2 : 4); ++r) {
+          if (r >= n) continue;
           const int b = first + r;
           // value codes of the block: columns of 4 tiles, tokens in pairs
           uint32_t vb[TG][4][2];
@@ -863,7 +864,6 @@ __device__ __forceinline__ void kv_attn_body(const KvLaunch &p, uint32_t *status
             }
           }
         }
-        first += n;
       }
       __syncwarp();  // every lane has read the stage
       fill();

@@ -43,9 +43,6 @@ struct KvRows {
 // Blocks of a launch for each SM (65536 tokens read: 90 us with 2, 67 with 8, 64 with 16).
 constexpr int kKvBlocks = 16;
 
-// Runs of blocks of a row.
-constexpr int kv_runs(int nb, bool q8) { return q8 ? nb / 2 + nb % 2 : nb / 4 + nb % 4 / 2 + nb % 2; }
-
 // What a thread works on, the same for all its tokens: quarter q of a run of a head.
 struct KvUnit {
   int head, q, first, n;  // the run's first block, its blocks
@@ -65,9 +62,8 @@ __device__ __forceinline__ KvUnit unit_of(int heads) {
   k.q = u & 3;
   const int run = (u >> 2) % kRuns;
   k.head = (u >> 2) / kRuns;
-  k.first = run * (Q8 ? 2 : 4);
-  if (!Q8 && NB % 4 == 3 && run == kRuns - 1) k.first = NB - 1;
-  k.n = kv_run(NB, Q8, min(k.first, NB - 1)).n;
+  k.first = kv_run_first(NB, Q8, run);
+  k.n = kv_run_blocks(NB, Q8, run);
   k.tok = static_cast<int64_t>(blockIdx.x) * per + slot;
   k.step = static_cast<int64_t>(gridDim.x) * per;
   k.there = slot < per && u < units && (units > 256 || blockIdx.z == 0);

@@ -52,6 +52,18 @@ __host__ __device__ constexpr KvRun kv_run(int nb, bool q8, int b) {
   return KvRun{first, n};
 }
 
+// The same by the run's number: plain arithmetic, which unrolled loops over runs
+// fold (a loop that steps by a run's length is not unrolled, and arrays indexed
+// in it lie in local memory).
+__host__ __device__ constexpr int kv_runs(int nb, bool q8) { return q8 ? nb / 2 + nb % 2 : nb / 4 + nb % 4 / 2 + nb % 2; }
+__host__ __device__ constexpr int kv_run_first(int nb, bool q8, int i) {
+  return q8 ? 2 * i : nb % 4 == 3 && i == nb / 4 + 1 ? nb - 1 : 4 * i;
+}
+__host__ __device__ constexpr int kv_run_blocks(int nb, bool q8, int i) {
+  const int left = nb - kv_run_first(nb, q8, i);
+  return !q8 && left >= 4 ? 4 : left >= 2 ? 2 : 1;
+}
+
 // Byte offset in the part of code byte x (ggml order: 32 of a Q8_0 block, 16 of
 // a Q4_0 block) of block b of token tok (0..15).
 __host__ __device__ constexpr int kv_key_code_at(int nb, bool q8, int tok, int b, int x) {
