@@ -67,6 +67,8 @@ _SIGS = {
     "qmm_kv_read": [_int, _int, _int, _i64, _i64, _i64, _int, _i64, _i64, _p, _p, _p, _p, _p],
     "qmm_kv_attn": [_int, _int, _int, _i64, _i64, _i64, _i64, _i64, _int, _i64, _i64, _p, _i64, _i64, _i64, _p, _p,
                     _i64, _i64, _p, _f32, _i64, _p, _p, _i64, _p],
+    "qmm_test_kv_withheld_copy": [_int, _int, _int, _i64, _i64, _i64, _i64, _i64, _int, _i64, _i64, _p, _i64, _i64, _i64,
+                                  _p, _p, _i64, _i64, _p, _f32, _i64, _p, _p, _i64, ctypes.c_uint64, _p],
     "qmm_kv_attn_workspace": [_i64, _i64, _i64, _i64, _i64, _p],
 }
 for _name, _args in _SIGS.items():

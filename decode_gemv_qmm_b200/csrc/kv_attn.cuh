@@ -487,7 +487,8 @@ __device__ __forceinline__ void kv_attn_body(const KvLaunch &p, uint32_t *status
       const int mine = lane - put_at;
       if (mine == 0) mbar_arrive_expect_tx(bar + st, __popc(ok) * C::kGroupBytes);
       __syncwarp();
-      if (mine >= 0 && mine < TG && (put_ok >> lane & 1))
+      const bool held = p.a.withhold && blockIdx.x == 0 && filled == 0;
+      if (mine >= 0 && mine < TG && (put_ok >> lane & 1) && !held)
         bulk_g2s(ring + st * C::kStageBytes + mine * C::kGroupBytes, src, C::kGroupBytes, bar + st, policy);
       ok_bits = (ok_bits & ~(((1u << TG) - 1) << (st * TG))) | ok << (st * TG);
       ++filled;
@@ -594,11 +595,11 @@ __device__ __forceinline__ void kv_attn_body(const KvLaunch &p, uint32_t *status
 
     for (int grp = use.first + use.a; grp < grp_end && !dead; grp += TG) {
       const int st = used % S;
-      if (!__all_sync(0xffffffffu, mbar_wait(bar + st, (used / S) & 1))) {
+      if (!__all_sync(0xffffffffu, mbar_wait(bar + st, (used / S) & 1, p.a.wait_ns))) {
         // Nothing more is copied; what is in flight is waited for once more. The
         // warp's items end with what they have, so that no block waits in vain.
         bool drained = true;
-        for (uint32_t i = used; i != filled; ++i) drained = mbar_wait(bar + i % S, (i / S) & 1) && drained;
+        for (uint32_t i = used; i != filled; ++i) drained = mbar_wait(bar + i % S, (i / S) & 1, p.a.wait_ns) && drained;
         if (lane == 0) atomicOr(status, kDevTimeoutFull | (drained ? 0u : kDevTimeoutDrain));
         dead = true;
         break;

@@ -9,6 +9,7 @@
 #include <string>
 
 #include "kv_layout.cuh"
+#include "qmm_common.cuh"
 #include "qmm_internal.h"
 
 namespace qmm {
@@ -498,8 +499,8 @@ static qmm_status kv_attn_impl(int ktype, int vtype, int dtype, int64_t B, int64
                                int64_t D, int block, int64_t pages, int64_t page, const void *Q, int64_t q_seq,
                                int64_t q_tok, int64_t q_head, const void *cache, const int32_t *table,
                                int64_t table_stride, int64_t max_pages, const int32_t *lens, float scale,
-                               int64_t window, void *Y, void *ws, int64_t ws_bytes, qmm_stream_t stream) {
-  const char *fn = "qmm_kv_attn";
+                               int64_t window, void *Y, void *ws, int64_t ws_bytes, qmm_stream_t stream, const char *fn,
+                               uint64_t wait_ns, bool withhold) {
   t_last_error.clear();
   KvForm f;
   QMM_TRY(check_kv_form(fn, ktype, vtype, Hkv, D, block, pages, page, &f));
@@ -545,6 +546,8 @@ static qmm_status kv_attn_impl(int ktype, int vtype, int dtype, int64_t B, int64
   a.max_pages = static_cast<int>(max_pages);
   a.window = window >= (int64_t(1) << 30) ? 0 : static_cast<int>(window);  // longer than any sequence: none
   a.scale = scale;
+  a.wait_ns = wait_ns;
+  a.withhold = withhold;
   return launch_kv_attn(dev, f, dtype, a, reinterpret_cast<cudaStream_t>(stream));
 }
 
@@ -708,7 +711,22 @@ QMM_API qmm_status qmm_kv_attn(int ktype, int vtype, int dtype, int64_t B, int64
                                int64_t table_stride, int64_t max_pages, const int32_t *lens, float scale,
                                int64_t window, void *Y, void *ws, int64_t ws_bytes, qmm_stream_t stream) {
   return kv_attn_impl(ktype, vtype, dtype, B, M, Hq, Hkv, D, block, pages, page, Q, q_seq, q_tok, q_head, cache, table,
-                      table_stride, max_pages, lens, scale, window, Y, ws, ws_bytes, stream);
+                      table_stride, max_pages, lens, scale, window, Y, ws, ws_bytes, stream, "qmm_kv_attn", kWaitLimitNs,
+                      false);
+}
+
+QMM_API qmm_status qmm_test_kv_withheld_copy(int ktype, int vtype, int dtype, int64_t B, int64_t M, int64_t Hq,
+                                             int64_t Hkv, int64_t D, int block, int64_t pages, int64_t page,
+                                             const void *Q, int64_t q_seq, int64_t q_tok, int64_t q_head,
+                                             const void *cache, const int32_t *table, int64_t table_stride,
+                                             int64_t max_pages, const int32_t *lens, float scale, int64_t window,
+                                             void *Y, void *ws, int64_t ws_bytes, uint64_t wait_ns,
+                                             qmm_stream_t stream) {
+  const char *fn = "qmm_test_kv_withheld_copy";
+  if (wait_ns < 1000 || wait_ns > 2000000000ull)
+    return set_error(QMM_ERR_SHAPE, "%s: wait_ns=%llu outside 1e3 .. 2e9", fn, (unsigned long long)wait_ns);
+  return kv_attn_impl(ktype, vtype, dtype, B, M, Hq, Hkv, D, block, pages, page, Q, q_seq, q_tok, q_head, cache, table,
+                      table_stride, max_pages, lens, scale, window, Y, ws, ws_bytes, stream, fn, wait_ns, true);
 }
 
 QMM_API qmm_status qmm_kv_attn_workspace(int64_t B, int64_t M, int64_t Hq, int64_t Hkv, int64_t D, int64_t *bytes) {

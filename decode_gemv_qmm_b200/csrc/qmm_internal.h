@@ -116,6 +116,8 @@ struct KvAttnArgs {
   int64_t q_seq, q_tok, q_head, table_stride;
   int batch, m, hq, max_pages, window;
   float scale;
+  uint64_t wait_ns;  // limit of a wait for a copy
+  bool withhold;     // failure-path test: the first copies of block 0's warps are never issued
 };
 qmm_status launch_kv_write(const DevInfo &dev, const KvForm &f, int dtype, int64_t T, const void *K, int64_t kst,
                            int64_t ksh, const void *V, int64_t vst, int64_t vsh, const int64_t *slots, void *cache,

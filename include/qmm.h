@@ -549,6 +549,21 @@ QMM_API qmm_status qmm_test_withheld_copy(int kernel, int64_t M, int64_t N, int6
                                           const void *X, float *Y, uint64_t wait_ns, qmm_stream_t stream);
 
 /*
+ * qmm_test_kv_withheld_copy -- the same for qmm_kv_attn (its arguments, and
+ * wait_ns): the first copies of block 0's warps are never issued. Those warps
+ * record it (bits 1 and 2), copy no more and end their items with what they have;
+ * the outputs of the items that block works on, at the beginning of the first
+ * sequences, are undefined, the others are computed as usual.
+ */
+QMM_API qmm_status qmm_test_kv_withheld_copy(int ktype, int vtype, int dtype, int64_t B, int64_t M, int64_t Hq,
+                                             int64_t Hkv, int64_t D, int block, int64_t pages, int64_t page,
+                                             const void *Q, int64_t q_seq, int64_t q_tok, int64_t q_head,
+                                             const void *cache, const int32_t *table, int64_t table_stride,
+                                             int64_t max_pages, const int32_t *lens, float scale, int64_t window,
+                                             void *Y, void *ws, int64_t ws_bytes, uint64_t wait_ns,
+                                             qmm_stream_t stream);
+
+/*
  * qmm_q4_gateup_unfused -- the unfused counterpart of qmm_q4_swiglu_gateup:
  * writes the gate and up projections G, U (M x N fp32 each) with two separate
  * projection launches, then Y = silu(G) * U with a third launch. Each

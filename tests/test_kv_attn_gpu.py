@@ -105,6 +105,119 @@ def test_many_sequences_of_uneven_lengths():
     c.check(c.run())
 
 
+@pytest.mark.parametrize("n,hkv,d,kt", [(33, 1, 64, 1), (257, 1, 64, 1), (700, 2, 64, 1), (300, 1, 256, 0), (129, 2, 256, 0)])
+def test_more_sequences_than_lanes_and_threads(n, hkv, d, kt):
+    """Sequences are looked up by lanes, then threads, then several a thread; empty ones lie in between."""
+    g = np.random.default_rng(n)
+    c = Case([int(v) for v in g.integers(0, 40, n) * g.integers(0, 2, n)], 1, hkv * 3, hkv, d, kt, kt, page=16, seed=n)
+    y = c.run()
+    c.check(y)
+    for s in range(n):
+        if not c.lens[s]:
+            assert (y[s] == 0).all()
+
+
+@pytest.mark.parametrize("batch", [1, 3, 40])
+def test_no_keys_anywhere(batch):
+    c = Case([0] * batch, 2, 4, 2, 64, 1, 1)
+    y = torch.full((batch, 2, 4, 64), float("nan"), device="cuda")
+    c.run(Y=y)
+    assert (y == 0).all() and qmm.device_status() == 0
+
+
+def test_one_scratch_for_calls_of_different_sizes():
+    """A scratch that other calls have used, larger and smaller, and one filled with ones or zeros."""
+    a = Case([4000, 10, 900], 1, 10, 2, 128, 1, 1, page=64, seed=21)
+    b = Case([700], 4, 16, 2, 128, 1, 1, page=64, seed=22, dtype=torch.bfloat16)
+    ws = torch.full((max(qmm.qmm_kv_attn_workspace(3, 1, 10, 2, 128), qmm.qmm_kv_attn_workspace(1, 4, 16, 2, 128)),), 255,
+                    dtype=torch.uint8, device="cuda")
+    wa, wb = a.run(), b.run()
+    for _ in range(3):
+        assert torch.equal(a.run(ws=ws), wa) and torch.equal(b.run(ws=ws), wb)
+    ws.zero_()
+    assert torch.equal(b.run(ws=ws), wb) and torch.equal(a.run(ws=ws), wa)
+
+
+def test_two_graphs_replayed_at_once():
+    """Each with the scratch of its own capture; replayed side by side on two streams, again and again."""
+    cases = [Case([3000, 900], 1, 10, 2, 128, 1, 1, page=64, seed=23), Case([1500, 2900], 1, 10, 2, 128, 1, 1, page=64, seed=24)]
+    want, graphs, outs, keep = [], [], [], []
+    for c in cases:
+        want.append(c.run())
+        t, n = dev(c.table), dev(np.array(c.lens, np.int32))
+        torch.cuda.synchronize()
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            outs.append(qmm.qmm_kv_attn(c.qd, c.cache, t, n, 2, scale=c.scale, **c.form))
+        graphs.append(g)
+        keep.append((t, n))
+    streams = [torch.cuda.Stream() for _ in cases]
+    for _ in range(20):
+        for o in outs:
+            o.fill_(float("nan"))
+        torch.cuda.synchronize()
+        for g, s in zip(graphs, streams):
+            with torch.cuda.stream(s):
+                g.replay()
+                g.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(o, w) for o, w in zip(outs, want))
+
+
+def test_first_call_of_a_process_is_captured():
+    """Nothing has to run before a capture."""
+    import subprocess
+    import sys
+    code = """
+import torch, decode_gemv_qmm_b200 as qmm
+f = dict(page=16)
+cache = torch.zeros(4, qmm.qmm_kv_page_bytes(2, 64, **f), dtype=torch.uint8, device="cuda")
+x = torch.randn(20, 2, 64, device="cuda"); slots = torch.arange(20, device="cuda")
+q = torch.randn(1, 1, 4, 64, device="cuda"); lens = torch.full((1,), 20, dtype=torch.int32, device="cuda")
+table = torch.arange(4, dtype=torch.int32, device="cuda").view(1, 4)
+torch.cuda.synchronize()
+g = torch.cuda.CUDAGraph()
+with torch.cuda.graph(g):
+    qmm.qmm_kv_write(cache, x, x, slots, **f)
+    k, v = qmm.qmm_kv_read(cache, slots, 2, 64, **f)
+    y = qmm.qmm_kv_attn(q, cache, table, lens, 2, **f)
+g.replay(); torch.cuda.synchronize()
+w = torch.softmax(torch.einsum("hd,nhd->hn", q[0, 0].double(), k.repeat_interleave(2, 1).double()) / 8, -1)
+assert torch.allclose(y[0, 0].double(), torch.einsum("hn,nhd->hd", w, v.repeat_interleave(2, 1).double()), atol=1e-5)
+assert qmm.device_status() == 0
+print("ok")
+"""
+    import os
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    r = subprocess.run([sys.executable, "-c", code], cwd=root, capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0 and r.stdout.strip().endswith("ok"), r.stderr[-2000:]
+
+
+def test_calls_from_threads_on_streams_of_their_own():
+    import threading
+    cases = [Case([500 + 300 * i, 20], 1, 10, 2, 128, 1, 1, page=64, seed=40 + i) for i in range(3)]
+    want = [c.run() for c in cases]
+    torch.cuda.synchronize()
+    bad = []
+
+    def work(i):
+        c, s = cases[i], torch.cuda.Stream()
+        t, n = dev(c.table), dev(np.array(c.lens, np.int32))
+        torch.cuda.synchronize()
+        for _ in range(20):
+            y = qmm.qmm_kv_attn(c.qd, c.cache, t, n, 2, scale=c.scale, stream=s, **c.form)
+            s.synchronize()
+            if not torch.equal(y, want[i]):
+                bad.append(i)
+
+    threads = [threading.Thread(target=work, args=(i,)) for i in range(3)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not bad
+
+
 @pytest.mark.parametrize("d,kt,vt,n", [(128, 1, 1, 40000), (64, 0, 0, 30011), (256, 1, 0, 9000)])
 def test_long_context_of_one_sequence(d, kt, vt, n):
     c = Case([n], 1, 5, 1, d, kt, vt, page=64, seed=n)

@@ -72,6 +72,37 @@ def test_prompts_of_any_length(t, page):
             assert np.array_equal(host(a), b.astype(np.float32))
 
 
+@pytest.mark.parametrize("hkv,d,kt,vt", [(64, 128, 0, 1), (100, 64, 1, 1), (33, 256, 0, 0), (1, 96, 1, 0)])
+def test_many_heads(hkv, d, kt, vt):
+    """More units of a token than a block has threads, for one of the two types or for both."""
+    g = np.random.default_rng(hkv)
+    t, page, pages = 7, 16, 2
+    k, kd = rows(g, t, hkv, d, torch.float32)
+    v, vd = rows(g, t, hkv, d, torch.float32)
+    slots = scatter(g, t, pages, page)
+    plain = ref.Cache(pages, hkv, d, page, kt, vt, fill=0x3C)
+    cache = dev(plain.bytes)
+    qmm.qmm_kv_write(cache, kd, vd, dev(slots), page=page, ktype=kt, vtype=vt)
+    plain.write(slots, k, v)
+    assert np.array_equal(host(cache), plain.bytes)
+    got = qmm.qmm_kv_read(cache, dev(slots), hkv, d, page=page, ktype=kt, vtype=vt)
+    for a, b in zip(got, plain.read(slots)):
+        assert np.array_equal(host(a), b.astype(np.float32))
+
+
+def test_bf16_blocks_with_ties():
+    """bf16 rows have many pairs of the same magnitude: the first of the largest decides, in every place."""
+    g = np.random.default_rng(12)
+    t, hkv, d = 64, 2, 128
+    x = torch.from_numpy(g.integers(-3, 4, (t, hkv, d)).astype(np.float32))
+    plain = ref.Cache(4, hkv, d, 16, 1, 1)
+    cache = dev(plain.bytes)
+    slots = np.arange(64)
+    qmm.qmm_kv_write(cache, x.bfloat16().cuda(), (-x).cuda().bfloat16(), dev(slots), page=16)
+    plain.write(slots, x.numpy(), -x.numpy())
+    assert np.array_equal(host(cache), plain.bytes)
+
+
 def test_strided_rows_slices_of_a_projection():
     g = np.random.default_rng(5)
     t, hkv, d, hq = 21, 2, 64, 14

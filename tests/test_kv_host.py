@@ -108,6 +108,12 @@ def test_refusals_before_any_cuda_call(call, kw, expect):
     assert lib.qmm_last_error_string()
 
 
+@pytest.mark.parametrize("wait_ns", [0, 999, 2_000_000_001])
+def test_withheld_copy_limits(wait_ns):
+    a = (1, 1, 0, 2, 1, 4, 2, 64, 32, 4, 64, P16, 256, 256, 64, P16, P16, 2, 2, P16, 1.0, 0, P16, P16, 1 << 40, wait_ns, 0)
+    assert lib.qmm_test_kv_withheld_copy(*a) == qmm.QMM_ERR_SHAPE
+
+
 def test_empty_calls():
     assert write(T=0, K=0, V=0, slots=0, cache=0) == 0
     assert read(T=0, K=0, V=0, slots=0, cache=0) == 0
