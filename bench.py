@@ -711,6 +711,9 @@ def run_case(spec: str, reps: int, seed: int):
     gateup:M:N:K        qmm_q4_swiglu_gateup
     prefill:q8|q4:M:N:K qmm_quant_matmul_prefill
     decode_step         the 121 GEMVs of one decode step
+    kvattn:KT:VT:DT:B:M:HQ:HKV:D:L   qmm_kv_attn, B sequences of L cached tokens (KT, VT q8|q4, DT f32|bf16)
+    kvwrite:KT:VT:DT:T:HKV:D         qmm_kv_write of T tokens
+    kvread:KT:VT:DT:T:HKV:D          qmm_kv_read of T tokens
     """
     import torch
 
@@ -768,6 +771,33 @@ def run_case(spec: str, reps: int, seed: int):
         X = torch.from_numpy(syn.act_bf16_bits(g, m, k).view(np.int16)).cuda()
         Y = torch.empty(m, n, device="cuda")
         launches.append(lambda: qmm.qmm_quant_matmul_prefill(wt, W, X, n, Y))
+    elif parts[0] in ("kvattn", "kvwrite", "kvread"):
+        types, dtype = {"q8": qmm.QMM_Q8_0, "q4": qmm.QMM_Q4_0}, {"f32": torch.float32, "bf16": torch.bfloat16}[parts[3]]
+        form = dict(page=64, ktype=types[parts[1]], vtype=types[parts[2]])
+        sizes = [int(v) for v in parts[4:]]
+        if parts[0] == "kvattn":
+            nseq, m, hq, hkv, d, length = sizes
+        else:
+            (tokens, hkv, d), nseq = sizes, 1
+            length = tokens
+        held = -(-length // 64)
+        cache = torch.empty(nseq * held, qmm.qmm_kv_page_bytes(hkv, d, **form), dtype=torch.uint8, device="cuda")
+        gen = torch.Generator(device="cuda").manual_seed(seed)
+        table = torch.randperm(nseq * held, generator=gen, device="cuda").int().view(nseq, held)
+        pos = torch.arange(length, device="cuda")
+        slots = (table.long()[:, pos // 64] * 64 + pos % 64).flatten()
+        for at in range(0, slots.numel(), 65536):
+            x = torch.randn(min(65536, slots.numel() - at), 2, hkv, d, generator=gen, device="cuda").to(dtype)
+            qmm.qmm_kv_write(cache, x[:, 0], x[:, 1], slots[at:at + 65536], **form)
+        if parts[0] == "kvattn":
+            q = torch.randn(nseq, m, hq, d, generator=gen, device="cuda").to(dtype)
+            lens = torch.full((nseq,), length, dtype=torch.int32, device="cuda")
+            launches.append(lambda: qmm.qmm_kv_attn(q, cache, table, lens, hkv, **form))
+        elif parts[0] == "kvwrite":
+            x = torch.randn(tokens, 2, hkv, d, generator=gen, device="cuda").to(dtype)
+            launches.append(lambda: qmm.qmm_kv_write(cache, x[:, 0], x[:, 1], slots, **form))
+        else:
+            launches.append(lambda: qmm.qmm_kv_read(cache, slots, hkv, d, dtype=dtype, **form))
     elif parts[0] == "decode_step":
         step = DecodeStep(seed, torch.device("cuda", 0), keep_host=False)
         launches.append(lambda: step.launch(qmm, torch.cuda.current_stream().cuda_stream, qmm.QMM_FLAG_EARLY_WEIGHTS))

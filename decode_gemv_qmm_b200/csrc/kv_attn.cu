@@ -56,7 +56,8 @@ qmm_status launch_kv_attn(const DevInfo &dev, const KvForm &f, int dtype, const 
 
 int64_t kv_attn_workspace_floats(int64_t batch, int m, int hq, int hkv, int d) {
   (void)batch;
-  return kv_attn_scratch_floats(8 * kv_attn_octets(d / 32, m * (hq / hkv), false), d);
+  const int rows = m * (hq / hkv), nb = d / 32;
+  return kv_attn_scratch_floats(8 * std::max(kv_attn_octets(nb, rows, false), kv_attn_octets(nb, rows, true)), d);
 }
 
 cudaError_t kv_attn_status(uint32_t *bits) {

@@ -79,10 +79,9 @@ __host__ __device__ constexpr int64_t kv_attn_slot_floats(int rows, int d) { ret
 
 constexpr int kKvMaxBlocks = 160;  // most blocks of a launch
 constexpr int kKvMaxWarps = 8;     // most warps of a block
-#ifndef KV_ITEM_COST
-#define KV_ITEM_COST 4
-#endif
-constexpr int kKvItemCost = KV_ITEM_COST;  // what beginning an item costs, in groups
+// What beginning an item costs a warp, in groups of keys (16 sequences of 6 to 100
+// tokens: 16 us with 4, 26 us with 2; 64 long ones: 103 and 106 us).
+constexpr int kKvItemCost = 4;
 
 // Scratch: two marks and two partial results of each block, two outputs of each warp.
 __host__ __device__ constexpr int64_t kv_attn_scratch_floats(int rows, int d) {
@@ -98,22 +97,15 @@ struct KvCfg {
   static constexpr int kTerms = FINE ? 2 : 1;             // fp16 terms of a query or weight
   static constexpr int kQBytes = OCT * NB * kTerms * 512;  // a warp's query fragments
   static constexpr int kBudget = 216 * 1024;  // of 227 KB; the rest is the static arrays
-#ifndef KV_TG1
-#define KV_TG1 4
-#endif
-#ifndef KV_TG2
-#define KV_TG2 2
-#endif
-#ifndef KV_TG4
-#define KV_TG4 1
-#endif
-#ifndef KV_NW
-#define KV_NW 8
-#endif
   static constexpr int warp_bytes(int tg, int stages) { return kQBytes + stages * tg * kGroupBytes; }
-  static constexpr int kNW = KV_NW * warp_bytes(1, 2) <= kBudget ? KV_NW : KV_NW / 2;
-  // groups of a step
-  static constexpr int kMaxTG = OCT == 1 ? KV_TG1 : OCT == 2 ? KV_TG2 : KV_TG4;
+  // Warps of a block, one block an SM. 12 and 16 warps of fewer registers and
+  // shorter steps were as fast or slower: instructions bound the kernel, not their
+  // latency.
+  static constexpr int kNW = 8 * warp_bytes(1, 2) <= kBudget ? 8 : 4;
+  // Groups of a step, as many as leave the sums in registers: 64 ragged sequences
+  // of up to 8192 tokens took 99, 105, 126 us with 4, 2, 1 (one octet of rows). A
+  // step's ring stage is 9 KB at most, so that two to four are in flight.
+  static constexpr int kMaxTG = OCT == 1 ? 4 : OCT == 2 ? 2 : 1;
   static constexpr bool fits(int tg) { return tg * kGroupBytes <= 9216 && kNW * warp_bytes(tg, 2) <= kBudget; }
   static constexpr int kTG = kMaxTG >= 4 && fits(4) ? 4 : kMaxTG >= 2 && fits(2) ? 2 : 1;
   static constexpr int stages() {
@@ -262,8 +254,18 @@ struct KvSum {
 // block scale multiplies the finished 32-dim dot in fp32; a value's block scale
 // goes into the weight, p d_v, in fp16 with the product's own remainder (FINE).
 // The weights change sides between the two products by 8 x 8 transposes. Each
-// step's sums are added to fp32 registers outside the tensor core, which does not
-// round its sums to nearest.
+// step's sums are added to fp32 registers outside the tensor core, whose own sums
+// need not be rounded to nearest.
+//
+// What bounds it: at short contexts the chain of latencies (7.6 us for 33 tokens
+// of two heads: 2 us to know the lengths and find the work, 1 us for the first
+// copies, 1 to 2 us a step and again for joining); at long ones instructions. 16
+// keys of a head of 128, Q4_0, fp32 queries, are 370 instructions of a warp: 132
+// on the 2-cycle ALU, 111 in fp16 (2 cycles), 32 products of 8 cycles in which,
+// measured, nothing else is issued, some 740 cycles together. One
+// sequence of 131072 tokens, 8 heads: 55 us, 2.7 TB/s of cache (29 us without the
+// arithmetic); 16 x 8192 tokens, 8 heads of 256, Q8_0, where a byte needs half the
+// instructions: 109 us, 5.2 TB/s, 80% of the measured copy rate.
 template <int NB, bool KQ8, bool VQ8, int OCT, bool FINE>
 __device__ __forceinline__ void kv_attn_body(const KvLaunch &p, uint32_t *status) {
   using C = KvCfg<NB, KQ8, VQ8, OCT, FINE>;
@@ -1032,11 +1034,14 @@ cudaError_t kv_attn_launch(const DevInfo &dev, KvLaunch &p, uint32_t *status, cu
   return cudaLaunchKernelEx(&cfg, kernel, p, status);
 }
 
-// Octets of rows that a warp takes at a time: the fewest that hold the rows, as
-// many at most as leave their sums in registers.
+// Octets of rows that a warp takes at a time: all of them while their sums stay
+// in registers, else two. 16 x 8192 keys of 8 heads of 128, Q4_0, took for 1, 2,
+// 3, 4 octets at a time 55, 87, 136, 188 us with fp32 queries (so four are better
+// as two and two) and 47, 67, 101, 130 us with bf16; five to eight as twos are
+// within 3% of the best split.
 constexpr int kv_attn_octets(int nb, int rows, bool fine) {
-  const int most = fine || nb > 4 ? 2 : 4, need = (rows + 7) / 8;
-  return need < most ? need : most;
+  const int need = (rows + 7) / 8, most = nb > 4 ? 2 : fine ? 3 : 4;
+  return need <= most ? need : 2;
 }
 
 template <int NB, bool KQ8, bool VQ8, bool FINE>
@@ -1045,7 +1050,7 @@ cudaError_t kv_attn_rows(const DevInfo &dev, KvLaunch &p, uint32_t *status, cons
     case 1: return kv_attn_launch<NB, KQ8, VQ8, 1, FINE>(dev, p, status, cfg);
     case 2: return kv_attn_launch<NB, KQ8, VQ8, 2, FINE>(dev, p, status, cfg);
     case 3:
-      if constexpr (NB <= 4 && !FINE) return kv_attn_launch<NB, KQ8, VQ8, 3, FINE>(dev, p, status, cfg);
+      if constexpr (NB <= 4) return kv_attn_launch<NB, KQ8, VQ8, 3, FINE>(dev, p, status, cfg);
       return cudaErrorInvalidValue;
     default:
       if constexpr (NB <= 4 && !FINE) return kv_attn_launch<NB, KQ8, VQ8, 4, FINE>(dev, p, status, cfg);

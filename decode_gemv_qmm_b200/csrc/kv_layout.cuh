@@ -36,25 +36,10 @@ constexpr int kKvGroup = 16;  // tokens of a group
 __host__ __device__ constexpr int kv_code_bytes(int nb, bool q8) { return nb * (q8 ? 512 : 256); }
 __host__ __device__ constexpr int kv_part_bytes(int nb, bool q8) { return kv_code_bytes(nb, q8) + nb * 32; }
 
-struct KvRun {
-  int first, n;  // first block of the run, its blocks
-};
-
-// The run of blocks that block b belongs to.
-__host__ __device__ constexpr KvRun kv_run(int nb, bool q8, int b) {
-  int first = 0, n = q8 ? 2 : 4;
-  while (b >= first + n || first + n > nb) {
-    if (first + n <= nb)
-      first += n;
-    else
-      n >>= 1;
-  }
-  return KvRun{first, n};
-}
-
-// The same by the run's number: plain arithmetic, which unrolled loops over runs
-// fold (a loop that steps by a run's length is not unrolled, and arrays indexed
-// in it lie in local memory).
+// The runs of blocks of a row: how many, a run's first block and its blocks. Plain
+// arithmetic on the run's number, which unrolled loops fold: a loop that steps by
+// a run's length is not unrolled, and arrays indexed in it lie in local memory
+// (attention over 16 x 8192 tokens of 8 heads of 256, Q8_0: 268 us, with this 109).
 __host__ __device__ constexpr int kv_runs(int nb, bool q8) { return q8 ? nb / 2 + nb % 2 : nb / 4 + nb % 4 / 2 + nb % 2; }
 __host__ __device__ constexpr int kv_run_first(int nb, bool q8, int i) {
   return q8 ? 2 * i : nb % 4 == 3 && i == nb / 4 + 1 ? nb - 1 : 4 * i;
@@ -62,22 +47,6 @@ __host__ __device__ constexpr int kv_run_first(int nb, bool q8, int i) {
 __host__ __device__ constexpr int kv_run_blocks(int nb, bool q8, int i) {
   const int left = nb - kv_run_first(nb, q8, i);
   return !q8 && left >= 4 ? 4 : left >= 2 ? 2 : 1;
-}
-
-// Byte offset in the part of code byte x (ggml order: 32 of a Q8_0 block, 16 of
-// a Q4_0 block) of block b of token tok (0..15).
-__host__ __device__ constexpr int kv_key_code_at(int nb, bool q8, int tok, int b, int x) {
-  const KvRun r = kv_run(nb, q8, b);
-  const int row = 8 * (tok >> 3) + 2 * (tok & 3) + ((tok >> 2) & 1);
-  if (q8) return r.first * 512 + ((row * 4 + (x & 15) / 4) * r.n + b - r.first) * 8 + (x >> 4) * 4 + (x & 3);
-  return r.first * 256 + ((row * 4 + x / 4) * r.n + b - r.first) * 4 + (x & 3);
-}
-
-__host__ __device__ constexpr int kv_val_code_at(int nb, bool q8, int tok, int b, int x) {
-  const KvRun r = kv_run(nb, q8, b);
-  const int g = (x & 15) >> 1, unit = q8 ? 4 : 2;
-  const int chunk = r.n * unit == 8 ? ((g >> 2) * 64 + tok * 4 + (g & 3)) * 8 : (tok * 8 + g) * r.n * unit;
-  return r.first * (q8 ? 512 : 256) + chunk + (b - r.first) * unit + (x >> 4) * 2 + (x & 1);
 }
 
 // Byte offset in the part of the fp16 scale of block b of token tok.
