@@ -562,9 +562,11 @@ __device__ __forceinline__ void kv_attn_body(const KvLaunch &p, uint32_t *status
       // exponent of the largest, at least -100 (smaller rows keep fewer bits of scores that are 0 anyway)
       const int ex = max(static_cast<int>(__float_as_uint(big) >> 23) - 127, -100);
       float up = __uint_as_float(static_cast<uint32_t>(14 - ex + 127) << 23);
+      // (at least the smallest normal number: times minus infinity it has to stay that)
       const float f = p.a.scale == 0.0f ? 1.0f
-                                        : fabsf(p.a.scale) * 1.44269504088896f *
-                                              __uint_as_float(static_cast<uint32_t>(ex - 14 + 127) << 23);
+                                        : fmaxf(fabsf(p.a.scale) * 1.44269504088896f *
+                                                    __uint_as_float(static_cast<uint32_t>(ex - 14 + 127) << 23),
+                                                1.17549435e-38f);
       factor[o] = make_float2(__shfl_sync(0xffffffffu, f, 8 * t), __shfl_sync(0xffffffffu, f, 8 * t + 4));
       if (p.a.scale <= 0.0f) up = p.a.scale < 0.0f ? -up : 0.0f;
 #pragma unroll

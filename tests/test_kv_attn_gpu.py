@@ -270,6 +270,18 @@ def test_scale_of_either_sign_and_zero():
         c.check(c.run(), f"scale {scale}")
 
 
+def test_query_rows_of_zeros():
+    """With any scale: equal weights over the keys a row sees, whatever lies behind them."""
+    for dtype in (torch.float32, torch.bfloat16):
+        c = Case([37, 5], 3, 4, 2, 64, 1, 0, seed=17, dtype=dtype)
+        c.qd = c.qd.clone()
+        c.qd[:, :, ::2] = 0
+        c.q = c.qd.double().cpu().numpy()
+        for scale in (0.125, 1e-12, 1e-38, -1e-30, 0.0):
+            c.scale = scale
+            c.check(c.run(), f"scale {scale}")
+
+
 def test_strided_queries_and_tables():
     c = Case([50, 20, 80], 2, 6, 2, 64, 1, 1, seed=6)
     want = c.run()
