@@ -85,7 +85,7 @@ constexpr int kKvItemCost = 4;
 
 // Scratch: two marks and two partial results of each block, two outputs of each warp.
 __host__ __device__ constexpr int64_t kv_attn_scratch_floats(int rows, int d) {
-  return kKvMaxBlocks * (4 + 2 * kv_attn_slot_floats(rows, d) + 2 * kKvMaxWarps * rows * d);
+  return kKvMaxBlocks * (4 + 2 * kv_attn_slot_floats(rows, d) + 2 * kKvMaxWarps * rows * (d + 8));
 }
 
 template <int NB, bool KQ8, bool VQ8, int OCT, bool FINE>
@@ -94,6 +94,7 @@ struct KvCfg {
   static constexpr int kKeyPart = kv_part_bytes(NB, KQ8);
   static constexpr int kGroupBytes = kKeyPart + kv_part_bytes(NB, VQ8);
   static constexpr int kRows = 8 * OCT;
+  static constexpr int kPiece = kRows * (kD + 8);         // floats of a warp's partial outputs (8 between rows: banks)
   static constexpr int kTerms = FINE ? 2 : 1;             // fp16 terms of a query or weight
   static constexpr int kQBytes = OCT * NB * kTerms * 512;  // a warp's query fragments
   static constexpr int kBudget = 216 * 1024;  // of 227 KB; the rest is the static arrays
@@ -110,14 +111,15 @@ struct KvCfg {
   static constexpr int kTG = kMaxTG >= 4 && fits(4) ? 4 : kMaxTG >= 2 && fits(2) ? 2 : 1;
   static constexpr int stages() {
     int n = 2;
-    while (n < 4 && kNW * warp_bytes(kTG, n + 1) <= kBudget) ++n;
+    while ((n < 4 || warp_bytes(kTG, n) < kPiece * 4) && kNW * warp_bytes(kTG, n + 1) <= kBudget) ++n;
     return n;
   }
   static constexpr int kStages = stages();
   static constexpr int kStageBytes = kTG * kGroupBytes;
   static constexpr int kSmem = kNW * warp_bytes(kTG, kStages);
   static_assert(kSmem <= kBudget, "stages do not fit");
-  static_assert(warp_bytes(kTG, kStages) >= kRows * kD * 4, "a warp's partial result does not fit");
+  static_assert(warp_bytes(kTG, kStages) >= kPiece * 4, "a warp's partial result does not fit");
+  static_assert(kStages * kTG <= 32, "a bit for each group in the ring");
   static_assert(kNW <= kKvMaxWarps, "scratch is sized for fewer warps");
 };
 
@@ -194,22 +196,6 @@ struct KvShare {
     return static_cast<int>(at < wide ? kv_div(at, each + 1) : more + kv_div(at - wide, each));
   }
 };
-
-// Reads of partial results, in shared memory or in the scratch, where another
-// block may have written them.
-__device__ __forceinline__ float2 kv_load2(const float *p) {
-  float2 v;
-  asm volatile("ld.relaxed.gpu.v2.f32 {%0, %1}, [%2];" : "=f"(v.x), "=f"(v.y) : "l"(p) : "memory");
-  return v;
-}
-__device__ __forceinline__ float4 kv_load4(const float *p) {
-  float4 v;
-  asm volatile("ld.relaxed.gpu.v4.f32 {%0, %1, %2, %3}, [%4];"
-               : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
-               : "l"(p)
-               : "memory");
-  return v;
-}
 
 // Four dims of a row, added up over partial results (maximum, sum; outputs), a
 // batch of them at a time so that their loads are in flight together.
@@ -366,7 +352,7 @@ __device__ __forceinline__ void kv_attn_body(const KvLaunch &p, uint32_t *status
   volatile uint64_t *marks = reinterpret_cast<volatile uint64_t *>(p.a.ws);  // two of each block
   constexpr int64_t kSlot = kv_attn_slot_floats(C::kRows, D);
   float *block_slots = p.a.ws + kKvMaxBlocks * 4 + 2 * blockIdx.x * kSlot;
-  float *warp_slots = p.a.ws + kKvMaxBlocks * (4 + 2 * kSlot) + 2 * NW * blockIdx.x * C::kRows * D;
+  float *warp_slots = p.a.ws + kKvMaxBlocks * (4 + 2 * kSlot) + 2 * NW * blockIdx.x * C::kPiece;
   if (blockIdx.x >= blocks) return;
   KvShare share;
   share.each = kv_div(total, blocks);
@@ -878,7 +864,7 @@ __device__ __forceinline__ void kv_attn_body(const KvLaunch &p, uint32_t *status
     const bool whole = use.a == 0 && use.b == use.n;
     const float down = __uint_as_float(static_cast<uint32_t>(127 - up_exp) << 23);
     const int piece = 2 * warp + (use.a == 0 ? 1 : 0);
-    float *kept = use.left <= 0 ? reinterpret_cast<float *>(own) : warp_slots + piece * C::kRows * D;
+    float *kept = use.left <= 0 ? reinterpret_cast<float *>(own) : warp_slots + piece * C::kPiece;
     if (!whole && lane == 0) pieces[piece] = Piece{use.seq, use.head, use.tile, use.a, use.b, use.n, kept};
     __syncwarp();
 #pragma unroll
@@ -897,7 +883,7 @@ __device__ __forceinline__ void kv_attn_body(const KvLaunch &p, uint32_t *status
         if (!whole && g == 0) piece_ml[piece][r] = make_float2(i ? top[o].y : top[o].x, li);
         const float by = whole ? (li > 0.0f ? down / li : 0.0f) : down;
         const int64_t out = kv_out_at(p, use.seq, use.head, row, D) + 2 * g;
-        float *part = kept + r * D + 2 * g;
+        float *part = kept + r * (D + 8) + 2 * g;
 #pragma unroll
         for (int n = 0; n < NB * 2; ++n) {  // half blocks
           const float2 x = acc[o][n / 2 * 4 + n % 2], y = acc[o][n / 2 * 4 + n % 2 + 2];
@@ -950,18 +936,17 @@ __device__ __forceinline__ void kv_attn_body(const KvLaunch &p, uint32_t *status
         float4 v[8];
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
-          const float *o, *m;
           if (phase == 0) {
             const int e = __ffs(left) - 1;
             if (left & (left - 1)) left &= left - 1;
-            o = pieces[e].out, m = &piece_ml[e][0].x;
+            ml[j] = piece_ml[e][r];
+            v[j] = *reinterpret_cast<const float4 *>(pieces[e].out + r * (D + 8) + d);
           } else {  // slot 1 of the first block, slot 0 of the others
             const int part = min(k + j, w.n - 1);
-            o = p.a.ws + kKvMaxBlocks * 4 + (2 * (static_cast<int>(w.pieces) + part) + (part == 0 ? 1 : 0)) * kSlot;
-            m = o + C::kRows * D;
+            const float *o = p.a.ws + kKvMaxBlocks * 4 + (2 * (static_cast<int>(w.pieces) + part) + (part == 0 ? 1 : 0)) * kSlot;
+            ml[j] = __ldcg(reinterpret_cast<const float2 *>(o + C::kRows * D + r * 2));
+            v[j] = __ldcg(reinterpret_cast<const float4 *>(o + r * D + d));
           }
-          ml[j] = kv_load2(m + r * 2);
-          v[j] = kv_load4(o + r * D + d);
           if (k + j >= w.n) ml[j].x = -INFINITY;
         }
         x.add(ml, v);
