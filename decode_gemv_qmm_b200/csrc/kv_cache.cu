@@ -194,12 +194,18 @@ __device__ __forceinline__ void write_units(const KvForm &f, int64_t tokens, con
       const float id = __shfl_sync(0xffffffffu, inverse, (threadIdx.x & 28) + j);
       uint32_t c[8];
 #pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        const float y = __fmul_rn(x[j][e], id);
-        if (Q8)  // half away from zero: the number below 0.5 takes halves up and nothing else; |y| < 127.5
-          c[e] = static_cast<uint32_t>(__float2int_rz(__fadd_rn(y, copysignf(0.49999997f, y))));
-        else  // truncated: the sum with 2^23, rounded towards zero, ends in the code
-          c[e] = __float_as_uint(__fadd_rz(fminf(__fadd_rn(y, 8.5f), 15.5f), 8388608.0f));
+      for (int e = 0; e < 8; e += 2) {
+        // The products one by one: a packed product before a packed sum gave other
+        // bytes for bf16 rows (as one rounding of both would), and each is rounded here.
+        const float2 y = make_float2(__fmul_rn(x[j][e], id), __fmul_rn(x[j][e + 1], id));
+        if (Q8) {  // half away from zero: the number below 0.5 takes halves up and nothing else; |y| < 127.5
+          c[e] = static_cast<uint32_t>(__float2int_rz(__fadd_rn(y.x, copysignf(0.49999997f, y.x))));
+          c[e + 1] = static_cast<uint32_t>(__float2int_rz(__fadd_rn(y.y, copysignf(0.49999997f, y.y))));
+        } else {  // truncated: the sum with 2^23, rounded towards zero, ends in the code
+          float2 z = __fadd2_rn(y, make_float2(8.5f, 8.5f));
+          z = __fadd2_rz(make_float2(fminf(z.x, 15.5f), fminf(z.y, 15.5f)), make_float2(8388608.0f, 8388608.0f));
+          c[e] = __float_as_uint(z.x), c[e + 1] = __float_as_uint(z.y);
+        }
       }
       const uint32_t lo = __byte_perm(__byte_perm(c[0], c[1], 0x0040), __byte_perm(c[2], c[3], 0x0040), 0x5410);
       const uint32_t hi = __byte_perm(__byte_perm(c[4], c[5], 0x0040), __byte_perm(c[6], c[7], 0x0040), 0x5410);
