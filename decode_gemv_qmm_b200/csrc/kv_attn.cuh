@@ -249,7 +249,7 @@ struct KvSum {
 // keys of a head of 128, Q4_0, fp32 queries, are 370 instructions of a warp: 132
 // on the 2-cycle ALU, 111 in fp16 (2 cycles), 32 products of 8 cycles in which,
 // measured, nothing else is issued, some 740 cycles together. One
-// sequence of 131072 tokens, 8 heads: 55 us, 2.7 TB/s of cache (29 us without the
+// sequence of 131072 tokens, 8 heads: 54 us, 2.8 TB/s of cache (29 us without the
 // arithmetic); 16 x 8192 tokens, 8 heads of 256, Q8_0, where a byte needs half the
 // instructions: 109 us, 5.2 TB/s, 80% of the measured copy rate.
 template <int NB, bool KQ8, bool VQ8, int OCT, bool FINE>

@@ -128,6 +128,8 @@ __device__ __forceinline__ void by_pairs(uint32_t (&w)[4], int n, bool val) {
     w[0] = __byte_perm(a, b, 0x5410), w[1] = __byte_perm(a, b, 0x7632);
 }
 
+// Bound by the conversions' instructions: 16384 tokens, 8 heads of 128, Q4_0,
+// bf16: 28.3 us (29.2 with the sums one by one; 29.3 with bf16 extremes in pairs).
 template <int NB, bool Q8, typename T>
 __device__ __forceinline__ void write_units(const KvForm &f, int64_t tokens, const T *rows, KvRows st, bool val,
                                             const int64_t *slots, uint8_t *cache) {
