@@ -197,6 +197,22 @@ struct KvShare {
   }
 };
 
+// Reads of partial results that another block wrote: the clobber keeps the
+// compiler from moving them over the wait for that block's mark.
+__device__ __forceinline__ float2 kv_load2(const float *p) {
+  float2 v;
+  asm volatile("ld.relaxed.gpu.global.v2.f32 {%0, %1}, [%2];" : "=f"(v.x), "=f"(v.y) : "l"(p) : "memory");
+  return v;
+}
+__device__ __forceinline__ float4 kv_load4(const float *p) {
+  float4 v;
+  asm volatile("ld.relaxed.gpu.global.v4.f32 {%0, %1, %2, %3}, [%4];"
+               : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+               : "l"(p)
+               : "memory");
+  return v;
+}
+
 // Four dims of a row, added up over partial results (maximum, sum; outputs), a
 // batch of them at a time so that their loads are in flight together.
 struct KvSum {
@@ -944,8 +960,8 @@ __device__ __forceinline__ void kv_attn_body(const KvLaunch &p, uint32_t *status
           } else {  // slot 1 of the first block, slot 0 of the others
             const int part = min(k + j, w.n - 1);
             const float *o = p.a.ws + kKvMaxBlocks * 4 + (2 * (static_cast<int>(w.pieces) + part) + (part == 0 ? 1 : 0)) * kSlot;
-            ml[j] = __ldcg(reinterpret_cast<const float2 *>(o + C::kRows * D + r * 2));
-            v[j] = __ldcg(reinterpret_cast<const float4 *>(o + r * D + d));
+            ml[j] = kv_load2(o + C::kRows * D + r * 2);
+            v[j] = kv_load4(o + r * D + d);
           }
           if (k + j >= w.n) ml[j].x = -INFINITY;
         }
