@@ -84,8 +84,12 @@ int64_t cache_pages(const char *fn, const at::Tensor &cache, int ktype, int vtyp
   return cache.size(0);
 }
 
+// The library takes addresses: those of tensors that are not on a CUDA device are kept from it.
+void on_cuda(const char *fn, const at::Device &dev) {
+  if (!dev.is_cuda()) refuse(fn, "the cache is on " + dev.str() + ", not on a CUDA device");
+}
+
 qmm_stream_t stream_of(const at::Device &dev) {
-  if (!dev.is_cuda()) return nullptr;  // (no such device: the library says so)
   return reinterpret_cast<qmm_stream_t>(c10::cuda::getCurrentCUDAStream(dev.index()).stream());
 }
 
@@ -113,7 +117,8 @@ PyObject *write(PyObject *const *a, Py_ssize_t n) {
   qmm_status st;
   const int64_t pages = cache_pages(fn, cache, ktype, vtype, K.size(1), K.size(2), block, page, &st);
   if (st != QMM_OK) return status(st);
-  const c10::OptionalDeviceGuard guard(dev.is_cuda() ? c10::optional<at::Device>(dev) : c10::nullopt);
+  on_cuda(fn, dev);
+  const c10::DeviceGuard guard(dev);
   st = qmm_kv_write(ktype, vtype, dtype, K.size(0), K.size(1), K.size(2), block, pages, page, K.data_ptr(), ks[0], ks[1],
                     V.data_ptr(), vs[0], vs[1], slots.data_ptr<int64_t>(), cache.data_ptr(), stream_of(dev));
   if (st != QMM_OK) return status(st);
@@ -134,7 +139,8 @@ PyObject *read(PyObject *const *a, Py_ssize_t n) {
   qmm_status st;
   const int64_t pages = cache_pages(fn, cache, ktype, vtype, heads, dim, block, page, &st);
   if (st != QMM_OK) return status(st);
-  const c10::OptionalDeviceGuard guard(dev.is_cuda() ? c10::optional<at::Device>(dev) : c10::nullopt);
+  on_cuda(fn, dev);
+  const c10::DeviceGuard guard(dev);
   at::Tensor out[2];
   for (int i = 0; i < 2; ++i) {
     PyObject *o = a[4 + i];
@@ -196,7 +202,8 @@ PyObject *attn(PyObject *const *a, Py_ssize_t n) {
       refuse(fn, "scale is not a number");
     }
   }
-  const c10::OptionalDeviceGuard guard(dev.is_cuda() ? c10::optional<at::Device>(dev) : c10::nullopt);
+  on_cuda(fn, dev);
+  const c10::DeviceGuard guard(dev);
   at::Tensor Y, ws;
   if (a[5] == Py_None) {
     Y = at::empty(Q.sizes(), cache.options().dtype(Q.scalar_type()));
