@@ -101,7 +101,9 @@ def _ptr(t) -> int:
         return 0
     if isinstance(t, int):
         return t
-    return t.data_ptr()
+    # A kernel cannot read pageable host memory: such a tensor is passed as NULL,
+    # which the library refuses wherever it needs the pointer.
+    return t.data_ptr() if t.is_cuda or t.is_pinned() else 0
 
 
 def _stream(stream) -> int:

@@ -25,3 +25,31 @@ def test_tensors_in_host_memory_are_refused(stream):
     for out in ((None, None), (q.clone(), ws)):
         with pytest.raises(ValueError, match="not on a CUDA device"):
             qmm.qmm_kv_attn(q, cache, table, lens, 2, *out, stream=stream, **FORM)
+
+
+def test_older_calls_pass_no_address_of_host_memory():
+    """The matmuls' entry points: the library is given NULL for a tensor in pageable host memory, and says so."""
+    w8, w4 = torch.zeros(4 * 2 * 34, dtype=torch.uint8), torch.zeros(4 * 2 * 18, dtype=torch.uint8)
+    x, q, d = torch.zeros(1, 64), torch.zeros(1, 64, dtype=torch.int8), torch.zeros(1, 2)
+    calls = [lambda: qmm.qmm_q8_gemv(w8, x, 4, stream=0),
+             lambda: qmm.qmm_q8_gemv(w8, x, 4, flags=qmm.QMM_FLAG_EARLY_WEIGHTS, stream=0),
+             lambda: qmm.qmm_quantize_act_q8_0(x, stream=0),
+             lambda: qmm.qmm_q8q8_gemv_q8_0(w8, w8[:68].view(1, 68), 64, 4, stream=0),
+             lambda: qmm.qmm_q8_gemv_auto(w8, x, 4, stream=0),
+             lambda: qmm.qmm_q8_gemv_multi([w8, w8], x, [4, 4], stream=0),
+             lambda: qmm.qmm_quantize_act_q8(x, stream=0),
+             lambda: qmm.qmm_q8q8_gemv(w8, q, d, 4, stream=0),
+             lambda: qmm.qmm_q8q8_gemv_fused(w8, x, 4, stream=0),
+             lambda: qmm.qmm_q8q8_block_dots(w8, q, 4, stream=0),
+             lambda: qmm.qmm_q8q8_gemv_fused_dots(w8, x, 4, stream=0),
+             lambda: qmm.qmm_q8q8_block_dots_q8_0(w8, w8[:68].view(1, 68), 64, 4, stream=0),
+             lambda: qmm.qmm_q4_gemv(w4, x, 4, stream=0),
+             lambda: qmm.qmm_q4_swiglu_gateup(w4, w4, x, 4, stream=0),
+             lambda: qmm.qmm_q4_gateup_unfused(w4, w4, x, 4, stream=0),
+             lambda: qmm.qmm_quant_matmul_prefill(0, w8, x.bfloat16(), 4, stream=0)]
+    for call in calls:
+        with pytest.raises(qmm.QmmError) as e:
+            call()
+        assert e.value.status == qmm.QMM_ERR_NULL
+    empty = torch.zeros(0, 4)
+    assert qmm.qmm_q8_gemv(w8, x[:0], 4, empty, stream=0) is empty
