@@ -23,7 +23,33 @@ if not os.path.exists(LIB_PATH):
 
 lib = ctypes.CDLL(LIB_PATH)
 
-from . import _qmm_bind  # noqa: E402  (built with the library; it links to it)
+
+def _load_bind():
+    """The native entry of the key/value cache's calls. It is built against one torch: under another, or without the
+    file, those calls raise an ImportError that says so, and every other call works."""
+    mark = os.path.join(_HERE, "_qmm_bind.so.torch")
+    try:
+        if os.path.exists(mark):
+            with open(mark) as f:
+                made_with = f.read()
+            if made_with != str(torch.__version__):
+                raise ImportError(f"built against torch {made_with}, this is {torch.__version__}")
+        from . import _qmm_bind
+        return _qmm_bind
+    except ImportError as e:
+        return _NoBind(f"decode_gemv_qmm_b200/_qmm_bind.so cannot be used ({e}); build it "
+                       "with `python decode_gemv_qmm_b200/build.py`")
+
+
+class _NoBind:
+    def __init__(self, why: str):
+        self._why = why
+
+    def __getattr__(self, name: str):
+        raise ImportError(self._why)
+
+
+_qmm_bind = _load_bind()
 
 QMM_OK, QMM_ERR_NULL, QMM_ERR_SHAPE, QMM_ERR_BLOCK, QMM_ERR_ALIGN = 0, 1, 2, 3, 4
 QMM_ERR_DTYPE, QMM_ERR_DEVICE, QMM_ERR_CUDA, QMM_ERR_DEVICE_CHECK = 5, 6, 7, 8

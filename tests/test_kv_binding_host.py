@@ -53,3 +53,34 @@ def test_older_calls_pass_no_address_of_host_memory():
         assert e.value.status == qmm.QMM_ERR_NULL
     empty = torch.zeros(0, 4)
     assert qmm.qmm_q8_gemv(w8, x[:0], 4, empty, stream=0) is empty
+
+
+@pytest.mark.parametrize("spoil", ["sys.modules['decode_gemv_qmm_b200._qmm_bind'] = None", "torch.__version__ = '1.0'"])
+def test_package_without_a_usable_binding(spoil):
+    """The native entry missing, or built against another torch: the other calls work, the cache's say what to do."""
+    import os
+    import subprocess
+    import sys
+    code = f"""
+import sys, torch
+{spoil}
+import decode_gemv_qmm_b200 as qmm
+assert qmm.version() and qmm.qmm_kv_page_bytes(2, 64, page=16) == 2 * 64 * 18
+try:
+    qmm.qmm_q8_gemv(torch.zeros(8, dtype=torch.uint8), torch.zeros(1, 33), 4, stream=0)
+except qmm.QmmError as e:
+    assert e.status == qmm.QMM_ERR_SHAPE
+x = torch.zeros(1, 2, 64)
+for call in (lambda: qmm.qmm_kv_write(x, x, x, x, page=16), lambda: qmm.qmm_kv_read(x, x, 2, 64, page=16),
+             lambda: qmm.qmm_kv_attn(x, x, x, x, 2, page=16)):
+    try:
+        call()
+    except ImportError as e:
+        assert "build.py" in str(e)
+    else:
+        raise AssertionError("no ImportError")
+print("ok")
+"""
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    r = subprocess.run([sys.executable, "-c", code], cwd=root, capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0 and r.stdout.strip() == "ok", r.stderr[-2000:]
