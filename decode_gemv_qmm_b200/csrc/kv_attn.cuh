@@ -235,6 +235,83 @@ struct KvSum {
   }
 };
 
+// yes ? a : b, as a selection of registers: the compiler makes a chain of them over an
+// array's elements an index into a copy of the array in local memory.
+__device__ __forceinline__ float2 choose(bool yes, float2 a, float2 b) {
+  float2 r;
+  asm("{.reg .pred p; setp.ne.s32 p, %6, 0; selp.f32 %0, %2, %4, p; selp.f32 %1, %3, %5, p;}"
+      : "=f"(r.x), "=f"(r.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "r"(static_cast<int>(yes)));
+  return r;
+}
+
+// Adds a step's weights times values to the sums, key by key in fp32, each key to the
+// rows that see it: a lane's rows are 8 o + 2t and the next, its dims those of its sums.
+// z: weights times 2^13, of rows 8 o + 2t and the next, for key (g >> 1) + 4 (g & 1) + 8 j
+// of group gi; acc: 2^up_exp times the sums; parts: the first group's values; ok: a bit
+// for each group that is there.
+template <int NB, bool VQ8, int kGroupBytes, int OCT, int TG>
+__device__ __forceinline__ void kv_add_keys(float2 (&acc)[OCT][NB * 4], const float2 (&z)[OCT][TG][2], uint32_t parts,
+                                            uint32_t ok, int key0, int up_exp, const int2 (&last)[OCT],
+                                            const int2 (&low)[OCT]) {
+  const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+  const float unit = __uint_as_float(static_cast<uint32_t>(up_exp - 13 + 127) << 23);
+#pragma unroll 1
+  for (int i = 0; i < TG * kKvGroup; ++i) {
+    const int key = key0 + i, tok = i % kKvGroup, from = 8 * (tok & 3) + (tok & 4) + t;
+    const bool there = ok >> (i / kKvGroup) & 1;
+    const uint32_t part = parts + i / kKvGroup * kGroupBytes;
+    float2 w[OCT];
+    bool seen_x[OCT], seen_y[OCT];
+#pragma unroll
+    for (int o = 0; o < OCT; ++o) {
+      w[o] = z[o][0][0];
+#pragma unroll
+      for (int h = 1; h < 2 * TG; ++h) w[o] = choose(i >> 3 == h, z[o][h >> 1][h & 1], w[o]);
+      w[o].x = __shfl_sync(0xffffffffu, w[o].x, from) * unit;
+      w[o].y = __shfl_sync(0xffffffffu, w[o].y, from) * unit;
+      seen_x[o] = there && key <= last[o].x && key >= low[o].x;
+      seen_y[o] = there && key <= last[o].y && key >= low[o].y;
+    }
+#pragma unroll
+    for (int run = 0; run < kv_runs(NB, VQ8); ++run) {
+      const int first = kv_run_first(NB, VQ8, run), n = kv_run_blocks(NB, VQ8, run), wide = VQ8 ? 4 : 2;
+      const uint32_t at = part + first * 128 * wide;
+      uint32_t vw[2] = {0u, 0u};
+      if (n * wide == 8) {
+        const uint2 v = lds_u2(at + ((g >> 2) * 64 + tok * 4 + (g & 3)) * 8);
+        vw[0] = v.x, vw[1] = v.y;
+      } else if (n * wide == 4) {
+        vw[0] = lds_u32(at + (tok * 8 + g) * 4);
+      } else {
+        vw[0] = lds_u16(at + (tok * 8 + g) * 2);
+      }
+#pragma unroll
+      for (int r = 0; r < (VQ8 ? 2 : 4); ++r) {
+        if (r >= n) continue;
+        const int b = first + r;
+        const uint32_t scale = lds_u16(part + kv_scale_at(NB, VQ8, tok, b));
+        const bool finite = (scale & 0x7c00u) != 0x7c00u;
+        const float d = half_bits_to_float(scale);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {  // dims 2g, 16 + 2g, 2g + 1, 17 + 2g
+          const int c = VQ8 ? static_cast<int8_t>(vw[r & 1] >> (8 * ((e & 1) * 2 + (e >> 1))))
+                            : static_cast<int>(vw[r >> 1] >> ((r & 1) * 16 + (e >> 1) * 8 + (e & 1) * 4) & 15u) - 8;
+          const float v = static_cast<float>(c) * d;
+#pragma unroll
+          for (int o = 0; o < OCT; ++o) {
+            float2 &a = acc[o][b * 4 + e];
+            if (finite)
+              a = make_float2(fmaf(w[o].x, v, a.x), fmaf(w[o].y, v, a.y));
+            else
+              a = make_float2(seen_x[o] ? a.x + v : a.x, seen_y[o] ? a.y + v : a.y);
+          }
+        }
+      }
+    }
+  }
+}
+
 // ---- the kernel -------------------------------------------------------------
 //
 // Work is a line on which the items, an item being (sequence, head, tile of
@@ -658,6 +735,7 @@ __device__ __forceinline__ void kv_attn_body(const KvLaunch &p, uint32_t *status
         for (int b = 0; b < NB; ++b) bits |= vs[gi][b][0] | vs[gi][b][1];
       bits = __reduce_or_sync(0xffffffffu, bits & 0x60006000u);
       int e_new = 13;
+      bool apart = false;  // products of this step lane by lane
       if (((bits | bits >> 16) & 0x6000u) != 0x2000u) {
         uint32_t big = 0;
 #pragma unroll
@@ -666,6 +744,7 @@ __device__ __forceinline__ void kv_attn_body(const KvLaunch &p, uint32_t *status
           for (int b = 0; b < NB; ++b)
             big = __vmaxu2(big, __vmaxu2(vs[gi][b][0] & 0x7fff7fffu, vs[gi][b][1] & 0x7fff7fffu));
         big = __reduce_max_sync(0xffffffffu, max(big & 0xffffu, big >> 16));
+        apart = big >= 0x7c00u;
         const int by = 14 - static_cast<int>(max(big >> 10, 1u));  // -17 .. 13: two factors of fp16
         e_new += by;
         const int by1 = by / 2, by2 = by - by1;
@@ -790,6 +869,7 @@ __device__ __forceinline__ void kv_attn_body(const KvLaunch &p, uint32_t *status
             float2 w = __ffma2_rn(z[o][gi][j], factor[o], from13);
             w = make_float2(exp2_approx(w.x), exp2_approx(w.y));
             add = __fadd2_rn(add, w);
+            z[o][gi][j] = w;
             if (FINE) {
               __half2 h, l;
               split_f16(w, h, l);
@@ -803,71 +883,81 @@ __device__ __forceinline__ void kv_attn_body(const KvLaunch &p, uint32_t *status
       }
 
       // ---- outputs ----
+      // A value that is not finite belongs to the rows that see it and to no other, but
+      // 0 times it in a matrix product is not 0.
+      if (apart) {
 #pragma unroll
-      for (int run = 0; run < kv_runs(NB, VQ8); ++run) {
-        const int first = kv_run_first(NB, VQ8, run), n = kv_run_blocks(NB, VQ8, run), wide = VQ8 ? 4 : 2, bytes = n * wide;
-        uint32_t vw[TG][4][2];
+        for (int o = 0; o < OCT; ++o)
 #pragma unroll
-        for (int gi = 0; gi < TG; ++gi)
+          for (int n = 0; n < NB * 4; ++n) acc[o][n] = make_float2(acc[o][n].x * keep[o].x, acc[o][n].y * keep[o].y);
+        kv_add_keys<NB, VQ8, C::kGroupBytes>(acc, z, stage + C::kKeyPart, ok, key0, e_new, last, low);
+      } else {
 #pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const uint32_t part = stage + gi * C::kGroupBytes + C::kKeyPart + first * 128 * wide;
-            if (bytes == 8) {
-              const uint2 v = lds_u2(part + ((g >> 2) * 64 + t * 4 + (g & 3)) * 8 + e * 128);
-              vw[gi][e][0] = v.x, vw[gi][e][1] = v.y;
-            } else if (bytes == 4) {
-              vw[gi][e][0] = lds_u32(part + (t * 8 + g) * 4 + e * 128);
-            } else {
-              vw[gi][e][0] = lds_u16(part + (t * 8 + g) * 2 + e * 64);
-            }
-          }
-#pragma unroll
-        for (int r = 0; r < (VQ8 ? 2 : 4); ++r) {
-          if (r >= n) continue;
-          const int b = first + r;
-          // value codes of the block: columns of 4 tiles, tokens in pairs
-          uint32_t vb[TG][4][2];
+        for (int run = 0; run < kv_runs(NB, VQ8); ++run) {
+          const int first = kv_run_first(NB, VQ8, run), n = kv_run_blocks(NB, VQ8, run), wide = VQ8 ? 4 : 2, bytes = n * wide;
+          uint32_t vw[TG][4][2];
 #pragma unroll
           for (int gi = 0; gi < TG; ++gi)
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {
-              if (VQ8) {
-                const uint32_t w0 = vw[gi][2 * h][r & 1] ^ 0x80808080u, w1 = vw[gi][2 * h + 1][r & 1] ^ 0x80808080u;
-                const uint32_t x = __byte_perm(w0, w1, 0x5140), y = __byte_perm(w0, w1, 0x7362);
-                vb[gi][0][h] = q8_pair<0x5150>(x, magic), vb[gi][2][h] = q8_pair<0x5352>(x, magic);
-                vb[gi][1][h] = q8_pair<0x5150>(y, magic), vb[gi][3][h] = q8_pair<0x5352>(y, magic);
+            for (int e = 0; e < 4; ++e) {
+              const uint32_t part = stage + gi * C::kGroupBytes + C::kKeyPart + first * 128 * wide;
+              if (bytes == 8) {
+                const uint2 v = lds_u2(part + ((g >> 2) * 64 + t * 4 + (g & 3)) * 8 + e * 128);
+                vw[gi][e][0] = v.x, vw[gi][e][1] = v.y;
+              } else if (bytes == 4) {
+                vw[gi][e][0] = lds_u32(part + (t * 8 + g) * 4 + e * 128);
               } else {
-                const uint32_t x = __byte_perm(vw[gi][2 * h][r >> 1], vw[gi][2 * h + 1][r >> 1], r & 1 ? 0x7632 : 0x5410);
-                const uint32_t x8 = x >> 8;
-                vb[gi][0][h] = q4_low(x, magic), vb[gi][1][h] = q4_high(x, magic);
-                vb[gi][2][h] = q4_low(x8, magic), vb[gi][3][h] = q4_high(x8, magic);
+                vw[gi][e][0] = lds_u16(part + (t * 8 + g) * 2 + e * 64);
               }
             }
 #pragma unroll
-          for (int o = 0; o < OCT; ++o) {
-            float4 c[2] = {make_float4(0.f, 0.f, 0.f, 0.f), make_float4(0.f, 0.f, 0.f, 0.f)};
-            uint32_t w[TG][TERMS][2];
+          for (int r = 0; r < (VQ8 ? 2 : 4); ++r) {
+            if (r >= n) continue;
+            const int b = first + r;
+            // value codes of the block: columns of 4 tiles, tokens in pairs
+            uint32_t vb[TG][4][2];
 #pragma unroll
             for (int gi = 0; gi < TG; ++gi)
 #pragma unroll
-              for (int j = 0; j < 2; ++j) {
-                const __half2 d = bits_h2(vs[gi][b][j]), hi = __hmul2(ph[o][gi][j], d);
-                w[gi][0][j] = h2_bits(hi);
-                if (FINE)  // p d_v = hi + what hi leaves of ph d_v + pl d_v
-                  w[gi][TERMS - 1][j] = h2_bits(__hfma2(pl[FINE ? o : 0][gi][j], d, __hfma2(ph[o][gi][j], d, __hneg2(hi))));
+              for (int h = 0; h < 2; ++h) {
+                if (VQ8) {
+                  const uint32_t w0 = vw[gi][2 * h][r & 1] ^ 0x80808080u, w1 = vw[gi][2 * h + 1][r & 1] ^ 0x80808080u;
+                  const uint32_t x = __byte_perm(w0, w1, 0x5140), y = __byte_perm(w0, w1, 0x7362);
+                  vb[gi][0][h] = q8_pair<0x5150>(x, magic), vb[gi][2][h] = q8_pair<0x5352>(x, magic);
+                  vb[gi][1][h] = q8_pair<0x5150>(y, magic), vb[gi][3][h] = q8_pair<0x5352>(y, magic);
+                } else {
+                  const uint32_t x = __byte_perm(vw[gi][2 * h][r >> 1], vw[gi][2 * h + 1][r >> 1], r & 1 ? 0x7632 : 0x5410);
+                  const uint32_t x8 = x >> 8;
+                  vb[gi][0][h] = q4_low(x, magic), vb[gi][1][h] = q4_high(x, magic);
+                  vb[gi][2][h] = q4_low(x8, magic), vb[gi][3][h] = q4_high(x8, magic);
+                }
               }
 #pragma unroll
-            for (int i = TERMS - 1; i >= 0; --i)
+            for (int o = 0; o < OCT; ++o) {
+              float4 c[2] = {make_float4(0.f, 0.f, 0.f, 0.f), make_float4(0.f, 0.f, 0.f, 0.f)};
+              uint32_t w[TG][TERMS][2];
 #pragma unroll
               for (int gi = 0; gi < TG; ++gi)
 #pragma unroll
-                for (int h = 0; h < 2; ++h)
-                  c[h] = mma_f16(make_uint4(vb[gi][2 * h][0], vb[gi][2 * h + 1][0], vb[gi][2 * h][1], vb[gi][2 * h + 1][1]),
-                                 w[gi][i][0], w[gi][i][1], c[h]);
+                for (int j = 0; j < 2; ++j) {
+                  const __half2 d = bits_h2(vs[gi][b][j]), hi = __hmul2(ph[o][gi][j], d);
+                  w[gi][0][j] = h2_bits(hi);
+                  if (FINE)  // p d_v = hi + what hi leaves of ph d_v + pl d_v
+                    w[gi][TERMS - 1][j] = h2_bits(__hfma2(pl[FINE ? o : 0][gi][j], d, __hfma2(ph[o][gi][j], d, __hneg2(hi))));
+                }
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {
-              acc[o][b * 4 + 2 * h] = __ffma2_rn(acc[o][b * 4 + 2 * h], keep[o], make_float2(c[h].x, c[h].y));
-              acc[o][b * 4 + 2 * h + 1] = __ffma2_rn(acc[o][b * 4 + 2 * h + 1], keep[o], make_float2(c[h].z, c[h].w));
+              for (int i = TERMS - 1; i >= 0; --i)
+#pragma unroll
+                for (int gi = 0; gi < TG; ++gi)
+#pragma unroll
+                  for (int h = 0; h < 2; ++h)
+                    c[h] = mma_f16(make_uint4(vb[gi][2 * h][0], vb[gi][2 * h + 1][0], vb[gi][2 * h][1], vb[gi][2 * h + 1][1]),
+                                   w[gi][i][0], w[gi][i][1], c[h]);
+#pragma unroll
+              for (int h = 0; h < 2; ++h) {
+                acc[o][b * 4 + 2 * h] = __ffma2_rn(acc[o][b * 4 + 2 * h], keep[o], make_float2(c[h].x, c[h].y));
+                acc[o][b * 4 + 2 * h + 1] = __ffma2_rn(acc[o][b * 4 + 2 * h + 1], keep[o], make_float2(c[h].z, c[h].w));
+              }
             }
           }
         }
@@ -952,18 +1042,19 @@ __device__ __forceinline__ void kv_attn_body(const KvLaunch &p, uint32_t *status
         float4 v[8];
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
+          ml[j] = make_float2(-INFINITY, 0.0f), v[j] = make_float4(0.f, 0.f, 0.f, 0.f);
+          if (k + j >= w.n) continue;  // (nothing in its place: results may be infinite)
           if (phase == 0) {
             const int e = __ffs(left) - 1;
-            if (left & (left - 1)) left &= left - 1;
+            left &= left - 1;
             ml[j] = piece_ml[e][r];
             v[j] = *reinterpret_cast<const float4 *>(pieces[e].out + r * (D + 8) + d);
           } else {  // slot 1 of the first block, slot 0 of the others
-            const int part = min(k + j, w.n - 1);
+            const int part = k + j;
             const float *o = p.a.ws + kKvMaxBlocks * 4 + (2 * (static_cast<int>(w.pieces) + part) + (part == 0 ? 1 : 0)) * kSlot;
             ml[j] = kv_load2(o + C::kRows * D + r * 2);
             v[j] = kv_load4(o + r * D + d);
           }
-          if (k + j >= w.n) ml[j].x = -INFINITY;
         }
         x.add(ml, v);
       }

@@ -460,7 +460,11 @@ QMM_API qmm_status qmm_kv_read(int ktype, int vtype, int dtype, int64_t T, int64
  *   Y[s][i][h] = sum_j p_j v_j / sum_j p_j,  p_j = exp(scale * (Q[s][i][h] . k_j) - max_j),
  *   over 0 <= j <= lens[s] - M + i and, if window > 0, j > lens[s] - M + i - window,
  * where query head h belongs to key/value head h / (Hq / Hkv). A row that sees
- * no key is 0. Cached tokens past lens[s] are never used, whatever they hold.
+ * no key is 0. Cached tokens past lens[s] are never used, whatever they hold;
+ * neither is, for a row, any other token that it does not see: a value that is
+ * not finite (an input above 524000 in magnitude has no finite Q4_0 scale)
+ * makes the outputs of its block infinite or NaN in the rows that see it, and
+ * in no other.
  *
  *   dtype     QMM_F32 or QMM_BF16: elements of Q and Y
  *   B, M      sequences (<= QMM_KV_MAX_BATCH) and query tokens of each
