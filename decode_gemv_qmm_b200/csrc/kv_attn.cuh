@@ -31,6 +31,15 @@ __device__ __forceinline__ float4 mma_f16(const uint4 &a, uint32_t b0, uint32_t 
   return d;
 }
 
+// The same with bf16 operands.
+__device__ __forceinline__ float4 mma_bf16(const uint4 &a, uint32_t b0, uint32_t b1, const float4 &c) {
+  float4 d;
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%11,%12,%13};"
+      : "=f"(d.x), "=f"(d.y), "=f"(d.z), "=f"(d.w)
+      : "r"(a.x), "r"(a.y), "r"(a.z), "r"(a.w), "r"(b0), "r"(b1), "f"(c.x), "f"(c.y), "f"(c.z), "f"(c.w));
+  return d;
+}
+
 // Two fp32 values as fp16 pairs hi + lo: 22 bits of each, when they are neither
 // above 65504 nor so small that lo falls below fp16's 2^-24.
 __device__ __forceinline__ void split_f16(float2 x, __half2 &hi, __half2 &lo) {
@@ -235,6 +244,45 @@ struct KvSum {
   }
 };
 
+// A run's value codes of a group, this lane's: two dims of each half block of tokens
+// t + 4 e, as many blocks as the run has.
+template <int NB, bool VQ8>
+__device__ __forceinline__ void kv_value_words(uint32_t (&vw)[4][2], uint32_t part, int run) {
+  const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+  const int wide = VQ8 ? 4 : 2, bytes = kv_run_blocks(NB, VQ8, run) * wide;
+  part += kv_run_first(NB, VQ8, run) * 128 * wide;
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    if (bytes == 8) {
+      const uint2 v = lds_u2(part + ((g >> 2) * 64 + t * 4 + (g & 3)) * 8 + e * 128);
+      vw[e][0] = v.x, vw[e][1] = v.y;
+    } else if (bytes == 4) {
+      vw[e][0] = lds_u32(part + (t * 8 + g) * 4 + e * 128);
+    } else {
+      vw[e][0] = lds_u16(part + (t * 8 + g) * 2 + e * 64);
+    }
+  }
+}
+
+// The codes of the run's block r as fp16: columns of 4 tiles, tokens in pairs.
+template <bool VQ8>
+__device__ __forceinline__ void kv_value_tiles(uint32_t (&vb)[4][2], const uint32_t (&vw)[4][2], int r, const KvMagic &magic) {
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    if (VQ8) {
+      const uint32_t w0 = vw[2 * h][r & 1] ^ 0x80808080u, w1 = vw[2 * h + 1][r & 1] ^ 0x80808080u;
+      const uint32_t x = __byte_perm(w0, w1, 0x5140), y = __byte_perm(w0, w1, 0x7362);
+      vb[0][h] = q8_pair<0x5150>(x, magic), vb[2][h] = q8_pair<0x5352>(x, magic);
+      vb[1][h] = q8_pair<0x5150>(y, magic), vb[3][h] = q8_pair<0x5352>(y, magic);
+    } else {
+      const uint32_t x = __byte_perm(vw[2 * h][r >> 1], vw[2 * h + 1][r >> 1], r & 1 ? 0x7632 : 0x5410);
+      const uint32_t x8 = x >> 8;
+      vb[0][h] = q4_low(x, magic), vb[1][h] = q4_high(x, magic);
+      vb[2][h] = q4_low(x8, magic), vb[3][h] = q4_high(x8, magic);
+    }
+  }
+}
+
 // yes ? a : b, as a selection of registers: the compiler makes a chain of them over an
 // array's elements an index into a copy of the array in local memory.
 __device__ __forceinline__ float2 choose(bool yes, float2 a, float2 b) {
@@ -245,71 +293,106 @@ __device__ __forceinline__ float2 choose(bool yes, float2 a, float2 b) {
   return r;
 }
 
-// Adds a step's weights times values to the sums, key by key in fp32, each key to the
-// rows that see it: a lane's rows are 8 o + 2t and the next, its dims those of its sums.
-// z: weights times 2^13, of rows 8 o + 2t and the next, for key (g >> 1) + 4 (g & 1) + 8 j
+__device__ __forceinline__ uint32_t bf2_bits(float2 x) {
+  const __nv_bfloat162 b = __float22bfloat162_rn(x);
+  return *reinterpret_cast<const uint32_t *>(&b);
+}
+
+// Adds a step's weights times values to the sums, whatever the values' scales: p d_v is
+// formed in fp32 and taken as three bf16 terms (24 bits, and fp32's range, so that no
+// weight loses bits to another); codes are exact in bf16 too. A weight of 0 takes
+// nothing from its value, infinite or NaN; weights of keys that a row sees are kept
+// from 0 where such a value is among them (`odd`), so that it gets there.
+// z: weights times 2^13 of rows 8 o + 2t and the next, for key (g >> 1) + 4 (g & 1) + 8 j
 // of group gi; acc: 2^up_exp times the sums; parts: the first group's values; ok: a bit
 // for each group that is there.
 template <int NB, bool VQ8, int kGroupBytes, int OCT, int TG>
-__device__ __forceinline__ void kv_add_keys(float2 (&acc)[OCT][NB * 4], const float2 (&z)[OCT][TG][2], uint32_t parts,
-                                            uint32_t ok, int key0, int up_exp, const int2 (&last)[OCT],
-                                            const int2 (&low)[OCT]) {
+__device__ __forceinline__ void kv_add_apart(float2 (&acc)[OCT][NB * 4], const float2 (&z)[OCT][TG][2], uint32_t parts,
+                                             uint32_t ok, int key0, int up_exp, bool odd, const int2 (&last)[OCT],
+                                             const int2 (&low)[OCT], const KvMagic &magic) {
   const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
   const float unit = __uint_as_float(static_cast<uint32_t>(up_exp - 13 + 127) << 23);
 #pragma unroll 1
-  for (int i = 0; i < TG * kKvGroup; ++i) {
-    const int key = key0 + i, tok = i % kKvGroup, from = 8 * (tok & 3) + (tok & 4) + t;
-    const bool there = ok >> (i / kKvGroup) & 1;
-    const uint32_t part = parts + i / kKvGroup * kGroupBytes;
-    float2 w[OCT];
-    bool seen_x[OCT], seen_y[OCT];
+  for (int gi = 0; gi < TG; ++gi) {
+    if (!(ok >> gi & 1)) continue;
+    const uint32_t part = parts + gi * kGroupBytes;
+    float2 w[OCT][2];  // transposed: row g, tokens t + 8 j and t + 4 + 8 j
 #pragma unroll
-    for (int o = 0; o < OCT; ++o) {
-      w[o] = z[o][0][0];
+    for (int o = 0; o < OCT; ++o)
 #pragma unroll
-      for (int h = 1; h < 2 * TG; ++h) w[o] = choose(i >> 3 == h, z[o][h >> 1][h & 1], w[o]);
-      w[o].x = __shfl_sync(0xffffffffu, w[o].x, from) * unit;
-      w[o].y = __shfl_sync(0xffffffffu, w[o].y, from) * unit;
-      seen_x[o] = there && key <= last[o].x && key >= low[o].x;
-      seen_y[o] = there && key <= last[o].y && key >= low[o].y;
-    }
+      for (int j = 0; j < 2; ++j) {
+        float2 x = z[o][0][j];
 #pragma unroll
-    for (int run = 0; run < kv_runs(NB, VQ8); ++run) {
-      const int first = kv_run_first(NB, VQ8, run), n = kv_run_blocks(NB, VQ8, run), wide = VQ8 ? 4 : 2;
-      const uint32_t at = part + first * 128 * wide;
-      uint32_t vw[2] = {0u, 0u};
-      if (n * wide == 8) {
-        const uint2 v = lds_u2(at + ((g >> 2) * 64 + tok * 4 + (g & 3)) * 8);
-        vw[0] = v.x, vw[1] = v.y;
-      } else if (n * wide == 4) {
-        vw[0] = lds_u32(at + (tok * 8 + g) * 4);
-      } else {
-        vw[0] = lds_u16(at + (tok * 8 + g) * 2);
+        for (int k = 1; k < TG; ++k) x = choose(k == gi, z[o][k][j], x);
+        x = make_float2(x.x * unit, x.y * unit);
+        if (odd) {
+          const int key = key0 + gi * kKvGroup + (g >> 1) + 4 * (g & 1) + 8 * j;
+          if (key <= last[o].x && key >= low[o].x) x.x = fmaxf(x.x, 1e-30f);
+          if (key <= last[o].y && key >= low[o].y) x.y = fmaxf(x.y, 1e-30f);
+        }
+        const uint32_t a = __float_as_uint(x.x), b = __float_as_uint(x.y);
+        const uint32_t up = h2_bits(transpose8(bits_h2(__byte_perm(a, b, 0x7632))));
+        const uint32_t down = h2_bits(transpose8(bits_h2(__byte_perm(a, b, 0x5410))));
+        w[o][j] = make_float2(__uint_as_float(__byte_perm(down, up, 0x5410)), __uint_as_float(__byte_perm(down, up, 0x7632)));
       }
 #pragma unroll
+    for (int run = 0; run < kv_runs(NB, VQ8); ++run) {
+      uint32_t vw[4][2];
+      kv_value_words<NB, VQ8>(vw, part, run);
+#pragma unroll
       for (int r = 0; r < (VQ8 ? 2 : 4); ++r) {
-        if (r >= n) continue;
-        const int b = first + r;
-        const uint32_t scale = lds_u16(part + kv_scale_at(NB, VQ8, tok, b));
-        const bool finite = (scale & 0x7c00u) != 0x7c00u;
-        const float d = half_bits_to_float(scale);
+        if (r >= kv_run_blocks(NB, VQ8, run)) continue;
+        const int b = kv_run_first(NB, VQ8, run) + r;
+        uint32_t vb[4][2];
+        kv_value_tiles<VQ8>(vb, vw, r, magic);
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {  // dims 2g, 16 + 2g, 2g + 1, 17 + 2g
-          const int c = VQ8 ? static_cast<int8_t>(vw[r & 1] >> (8 * ((e & 1) * 2 + (e >> 1))))
-                            : static_cast<int>(vw[r >> 1] >> ((r & 1) * 16 + (e >> 1) * 8 + (e & 1) * 4) & 15u) - 8;
-          const float v = static_cast<float>(c) * d;
+        for (int i = 0; i < 4; ++i)
 #pragma unroll
-          for (int o = 0; o < OCT; ++o) {
-            float2 &a = acc[o][b * 4 + e];
-            if (finite)
-              a = make_float2(fmaf(w[o].x, v, a.x), fmaf(w[o].y, v, a.y));
-            else
-              a = make_float2(seen_x[o] ? a.x + v : a.x, seen_y[o] ? a.y + v : a.y);
+          for (int j = 0; j < 2; ++j) vb[i][j] = bf2_bits(__half22float2(bits_h2(vb[i][j])));
+        const uint2 scales = lds_u2(part + kv_scale_at(NB, VQ8, t, b));
+#pragma unroll
+        for (int o = 0; o < OCT; ++o) {
+          uint32_t terms[3][2];
+#pragma unroll
+          for (int j = 0; j < 2; ++j) {
+            const float2 d = __half22float2(bits_h2(j ? scales.y : scales.x));
+            float2 x = make_float2(w[o][j].x != 0.0f ? w[o][j].x * d.x : 0.0f, w[o][j].y != 0.0f ? w[o][j].y * d.y : 0.0f);
+#pragma unroll
+            for (int i = 0; i < 3; ++i) {
+              const uint32_t y = bf2_bits(x);
+              terms[i][j] = y;
+              // (an infinity is its own first term)
+              x.x = isinf(x.x) ? 0.0f : x.x - __uint_as_float(y << 16);
+              x.y = isinf(x.y) ? 0.0f : x.y - __uint_as_float(y & 0xffff0000u);
+            }
+          }
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            float4 c = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+            for (int i = 2; i >= 0; --i)
+              c = mma_bf16(make_uint4(vb[2 * h][0], vb[2 * h + 1][0], vb[2 * h][1], vb[2 * h + 1][1]), terms[i][0], terms[i][1], c);
+            float2 &p = acc[o][b * 4 + 2 * h], &q = acc[o][b * 4 + 2 * h + 1];
+            p = make_float2(p.x + c.x, p.y + c.y), q = make_float2(q.x + c.z, q.y + c.w);
           }
         }
       }
     }
   }
+}
+
+// The same as a call, its arrays in local memory: for two octets of heads of 192 and 256,
+// whose sums leave no registers for it in the middle of a step (16 rows of 256, Q8_0,
+// fp32, 8 x 8192 keys of 8 heads, no step of which calls it: 168 us in line, 151 so).
+template <int NB, int OCT, int TG>
+struct KvApart {
+  float2 acc[OCT][NB * 4], z[OCT][TG][2];
+  int2 last[OCT], low[OCT];
+};
+template <int NB, bool VQ8, int kGroupBytes, int OCT, int TG>
+__device__ __noinline__ void kv_add_apart_call(KvApart<NB, OCT, TG> &s, uint32_t parts, uint32_t ok, int key0, int up_exp,
+                                               bool odd, const KvMagic &magic) {
+  kv_add_apart<NB, VQ8, kGroupBytes>(s.acc, s.z, parts, ok, key0, up_exp, odd, s.last, s.low, magic);
 }
 
 // ---- the kernel -------------------------------------------------------------
@@ -674,6 +757,11 @@ __device__ __forceinline__ void kv_attn_body(const KvLaunch &p, uint32_t *status
     __syncwarp();
     const int low_all = p.a.window > 0 ? max(0, use.len - p.a.m - p.a.window + 1) : 0;
     const int grp_end = use.first + use.b;
+    // a lane's 16 bytes of a step's value scales
+    constexpr int kLooks = TG * NB * 2;
+    static_assert(kLooks <= 32, "a step's value scales in one load of a warp");
+    const int look = lane % kLooks;
+    const uint32_t look_off = look / (2 * NB) * C::kGroupBytes + C::kKeyPart + kv_code_bytes(NB, VQ8) + look % (2 * NB) * 16;
     int up_exp = 13;  // acc and sum are 2^up_exp and 2^13 times the outputs' and weights' sums
 
     for (int grp = use.first + use.a; grp < grp_end && !dead; grp += TG) {
@@ -726,36 +814,58 @@ __device__ __forceinline__ void kv_attn_body(const KvLaunch &p, uint32_t *status
           }
       }
       // The weights are p 2^13 and so p d_v 2^13: inside fp16 with room for both
-      // terms while the largest scale is in [2^-7, 2). Outside, the scales of the
-      // step are brought there by a power of two, which the sums keep (up_exp).
-      uint32_t bits = 0;
-#pragma unroll
-      for (int gi = 0; gi < TG; ++gi)
-#pragma unroll
-        for (int b = 0; b < NB; ++b) bits |= vs[gi][b][0] | vs[gi][b][1];
-      bits = __reduce_or_sync(0xffffffffu, bits & 0x60006000u);
+      // terms while every scale is in [2^-7, 2), or 0. Scales that lie within 8
+      // binades of each other are brought there by a power of two, exactly, which the
+      // sums keep (up_exp). Others, and scales that are not finite, would lose bits
+      // to the largest of them, or reach rows that must not see them: see `apart`.
+      // To look at them all, a lane takes 16 bytes: of two blocks' (of one or two of
+      // the four token columns t), tokens t, t + 4, t + 8 and t + 12.
+      uint4 d = *reinterpret_cast<const uint4 *>(ring + st * C::kStageBytes + look_off);
       int e_new = 13;
-      bool apart = false;  // products of this step lane by lane
-      if (((bits | bits >> 16) & 0x6000u) != 0x2000u) {
-        uint32_t big = 0;
+      bool apart = false, odd = false;  // scales far apart, or not finite
+      if (__any_sync(0xffffffffu, !full || ((d.x | d.y | d.z | d.w) & 0x40004000u) | (~(d.x & d.y & d.z & d.w) & 0x20002000u))) {
+        if (!full) {  // (as above)
 #pragma unroll
-        for (int gi = 0; gi < TG; ++gi)
+          for (int i = 0; i < 2; ++i) {
+            const int unit = look % (2 * NB) * 2 + i, grp_i = look / (2 * NB);
+            uint32_t *w = i ? &d.z : &d.x;
 #pragma unroll
-          for (int b = 0; b < NB; ++b)
-            big = __vmaxu2(big, __vmaxu2(vs[gi][b][0] & 0x7fff7fffu, vs[gi][b][1] & 0x7fff7fffu));
+            for (int e = 0; e < 4; ++e) {
+              const int key = key0 + grp_i * kKvGroup + unit / NB + 4 * e;
+              if (!(ok >> grp_i & 1) || key >= use.len || key < low_all) w[e >> 1] &= e & 1 ? 0x0000ffffu : 0xffff0000u;
+            }
+          }
+        }
+        uint32_t big = 0, small = ~0u;  // small: less 1, so that 0 is the largest
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const uint32_t x = (&d.x)[i] & 0x7fff7fffu;
+          big = __vmaxu2(big, x), small = __vminu2(small, __vsub2(x, 0x00010001u));
+        }
         big = __reduce_max_sync(0xffffffffu, max(big & 0xffffu, big >> 16));
-        apart = big >= 0x7c00u;
-        const int by = 14 - static_cast<int>(max(big >> 10, 1u));  // -17 .. 13: two factors of fp16
-        e_new += by;
-        const int by1 = by / 2, by2 = by - by1;
-        const uint32_t f1 = static_cast<uint32_t>(by1 + 15) << 10, f2 = static_cast<uint32_t>(by2 + 15) << 10;
+        small = __reduce_min_sync(0xffffffffu, min(small & 0xffffu, small >> 16)) + 1;
+        // exponents -24 .. 15, of subnormal numbers too; 128 of infinities and NaN
+        const int most = static_cast<int>(__float_as_uint(half_bits_to_float(big)) >> 23) - 127;
+        const int least = static_cast<int>(__float_as_uint(half_bits_to_float(small)) >> 23) - 127;
+        odd = most > 15;
+        apart = odd || (big != 0 && most - least > 7);
+        if (big == 0 || apart) {
+          e_new = up_exp;
+        } else if (most > 1 || least < -7) {  // (p d_v 2^13 is below 2^15 up to here)
+          const auto times = [&](int by) {
+            const uint32_t f = static_cast<uint32_t>(by + 15) << 10;
 #pragma unroll
-        for (int gi = 0; gi < TG; ++gi)
+            for (int gi = 0; gi < TG; ++gi)
 #pragma unroll
-          for (int b = 0; b < NB; ++b)
+              for (int b = 0; b < NB; ++b)
 #pragma unroll
-            for (int h = 0; h < 2; ++h)
-              vs[gi][b][h] = h2_bits(__hmul2(__hmul2(bits_h2(vs[gi][b][h]), bits_h2(f1 | f1 << 16)), bits_h2(f2 | f2 << 16)));
+                for (int h = 0; h < 2; ++h) vs[gi][b][h] = h2_bits(__hmul2(bits_h2(vs[gi][b][h]), bits_h2(f | f << 16)));
+          };
+          e_new = 13 - most;
+          const int by = max(-14, min(15, -most));  // (2^by is a normal fp16 number)
+          times(by);
+          if (by != -most) times(-most - by);
+        }
       }
 
       // ---- scores ----
@@ -883,33 +993,42 @@ __device__ __forceinline__ void kv_attn_body(const KvLaunch &p, uint32_t *status
       }
 
       // ---- outputs ----
-      // A value that is not finite belongs to the rows that see it and to no other, but
-      // 0 times it in a matrix product is not 0.
+      // Scales of sizes far apart: in fp16 the small ones' weights would keep few bits,
+      // whichever rows and dims the large ones belong to. And a value that is not
+      // finite belongs to the rows that see it and to no other, but 0 times it in a
+      // matrix product is not 0. (16 x 8192 keys of 8 heads of 128, Q4_0, fp32: 86 us
+      // where every step is like that, 55 us where none is.)
       if (apart) {
 #pragma unroll
         for (int o = 0; o < OCT; ++o)
 #pragma unroll
           for (int n = 0; n < NB * 4; ++n) acc[o][n] = make_float2(acc[o][n].x * keep[o].x, acc[o][n].y * keep[o].y);
-        kv_add_keys<NB, VQ8, C::kGroupBytes>(acc, z, stage + C::kKeyPart, ok, key0, e_new, last, low);
+        if constexpr (NB > 4 && OCT > 1) {
+          KvApart<NB, OCT, TG> s;
+#pragma unroll
+          for (int o = 0; o < OCT; ++o) {
+            s.last[o] = last[o], s.low[o] = low[o];
+#pragma unroll
+            for (int n = 0; n < NB * 4; ++n) s.acc[o][n] = acc[o][n];
+#pragma unroll
+            for (int gi = 0; gi < TG; ++gi) s.z[o][gi][0] = z[o][gi][0], s.z[o][gi][1] = z[o][gi][1];
+          }
+          kv_add_apart_call<NB, VQ8, C::kGroupBytes>(s, stage + C::kKeyPart, ok, key0, e_new, odd, magic);
+#pragma unroll
+          for (int o = 0; o < OCT; ++o)
+#pragma unroll
+            for (int n = 0; n < NB * 4; ++n) acc[o][n] = s.acc[o][n];
+        } else {
+          kv_add_apart<NB, VQ8, C::kGroupBytes>(acc, z, stage + C::kKeyPart, ok, key0, e_new, odd, last, low, magic);
+        }
       } else {
 #pragma unroll
         for (int run = 0; run < kv_runs(NB, VQ8); ++run) {
-          const int first = kv_run_first(NB, VQ8, run), n = kv_run_blocks(NB, VQ8, run), wide = VQ8 ? 4 : 2, bytes = n * wide;
+          const int first = kv_run_first(NB, VQ8, run), n = kv_run_blocks(NB, VQ8, run);
           uint32_t vw[TG][4][2];
 #pragma unroll
           for (int gi = 0; gi < TG; ++gi)
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              const uint32_t part = stage + gi * C::kGroupBytes + C::kKeyPart + first * 128 * wide;
-              if (bytes == 8) {
-                const uint2 v = lds_u2(part + ((g >> 2) * 64 + t * 4 + (g & 3)) * 8 + e * 128);
-                vw[gi][e][0] = v.x, vw[gi][e][1] = v.y;
-              } else if (bytes == 4) {
-                vw[gi][e][0] = lds_u32(part + (t * 8 + g) * 4 + e * 128);
-              } else {
-                vw[gi][e][0] = lds_u16(part + (t * 8 + g) * 2 + e * 64);
-              }
-            }
+            kv_value_words<NB, VQ8>(vw[gi], stage + gi * C::kGroupBytes + C::kKeyPart, run);
 #pragma unroll
           for (int r = 0; r < (VQ8 ? 2 : 4); ++r) {
             if (r >= n) continue;
@@ -918,20 +1037,7 @@ __device__ __forceinline__ void kv_attn_body(const KvLaunch &p, uint32_t *status
             uint32_t vb[TG][4][2];
 #pragma unroll
             for (int gi = 0; gi < TG; ++gi)
-#pragma unroll
-              for (int h = 0; h < 2; ++h) {
-                if (VQ8) {
-                  const uint32_t w0 = vw[gi][2 * h][r & 1] ^ 0x80808080u, w1 = vw[gi][2 * h + 1][r & 1] ^ 0x80808080u;
-                  const uint32_t x = __byte_perm(w0, w1, 0x5140), y = __byte_perm(w0, w1, 0x7362);
-                  vb[gi][0][h] = q8_pair<0x5150>(x, magic), vb[gi][2][h] = q8_pair<0x5352>(x, magic);
-                  vb[gi][1][h] = q8_pair<0x5150>(y, magic), vb[gi][3][h] = q8_pair<0x5352>(y, magic);
-                } else {
-                  const uint32_t x = __byte_perm(vw[gi][2 * h][r >> 1], vw[gi][2 * h + 1][r >> 1], r & 1 ? 0x7632 : 0x5410);
-                  const uint32_t x8 = x >> 8;
-                  vb[gi][0][h] = q4_low(x, magic), vb[gi][1][h] = q4_high(x, magic);
-                  vb[gi][2][h] = q4_low(x8, magic), vb[gi][3][h] = q4_high(x8, magic);
-                }
-              }
+              kv_value_tiles<VQ8>(vb[gi], vw[gi], r, magic);
 #pragma unroll
             for (int o = 0; o < OCT; ++o) {
               float4 c[2] = {make_float4(0.f, 0.f, 0.f, 0.f), make_float4(0.f, 0.f, 0.f, 0.f)};

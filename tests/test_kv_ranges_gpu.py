@@ -107,3 +107,88 @@ def test_scales_that_are_not_finite(bits, vt):
     take(c, 1, d)
     assert not np.isfinite(c.kv[0][1][n - 2, 0, 64:96]).any() and np.isfinite(c.kv[0][1][n - 2, 0, :64]).all()
     check_rows(c, c.run(), hex(bits))
+
+
+@pytest.mark.parametrize("vt", [0, 1])
+@pytest.mark.parametrize("d", [64, 96, 128, 192, 256])
+def test_nothing_but_infinities(d, vt):
+    """Every scale that a step holds, alone and between tokens of the usual size."""
+    g = np.random.default_rng(2)
+    for n, odd in ((1, [0]), (3, [0, 1, 2]), (64, range(64)), (130, range(64, 128)), (131, [130])):
+        c = Case([n], 2, 18 if d < 256 else 9, 1, d, 1, vt, seed=n)
+        v = g.standard_normal((n, 1, d))
+        v[list(odd)] = 1e9 * (1 + g.random((len(odd), 1, d)))
+        refill(c, g.standard_normal((n, 1, d)), v)
+        check_rows(c, c.run(), f"{n} tokens")
+
+
+@pytest.mark.parametrize("vt", [0, 1])
+@pytest.mark.parametrize("big", [1, 4, 8, 11, 16, 20])
+def test_a_large_block_beside_small_ones(big, vt):
+    """32 dims 2^big in size, the others 2^-7: each block's outputs are as near as its own values allow."""
+    n, d = 150, 128
+    g = np.random.default_rng(big)
+    for at in (0, 64):
+        c = Case([n], 2, 4, 1, d, 1, vt, seed=5)
+        v = g.standard_normal((n, 1, d)) * 2.0 ** -7
+        v[..., at:at + 32] *= 2.0 ** (big + 7 - (4 if big > 15 else 0))
+        refill(c, g.standard_normal((n, 1, d)), v)
+        check_rows(c, c.run(), f"2^{big}, dims {at}")
+
+
+@pytest.mark.parametrize("vt", [0, 1])
+@pytest.mark.parametrize("size", [2.0 ** 8, 2.0 ** 14, 2.0 ** 18])
+def test_a_large_token_hidden_from_some_rows(size, vt):
+    """The window leaves token 22 to the first two of four rows, or the causal limit the last token to the last row."""
+    g = np.random.default_rng(6)
+    for window, at in ((40, 22), (0, 63)):
+        c = Case([64], 4, 4, 1, 64, 1, vt, window=window, seed=12)
+        v = g.standard_normal((64, 1, 64)) * 2.0 ** -8
+        v[at] *= size
+        refill(c, g.standard_normal((64, 1, 64)), v)
+        low = max(0, 63 - window + 1) if window else 0
+        assert at < low if window else at > 62
+        check_rows(c, c.run(), f"window {window}")
+
+
+@pytest.mark.parametrize("vt", [0, 1])
+@pytest.mark.parametrize("down", [0.0, 4.0, 12.0, 30.0])
+def test_a_large_token_of_little_weight(down, vt):
+    """Seen by all, 2^22 times the others' size, with a weight of about exp(-down) of theirs."""
+    n, d = 64, 128
+    g = np.random.default_rng(7)
+    c = Case([n], 1, 4, 1, d, 0, vt, seed=8)
+    c.qd = torch.ones_like(c.qd)
+    c.q = c.qd.double().cpu().numpy()
+    k = g.standard_normal((n, 1, d)) * 0.01
+    v = g.standard_normal((n, 1, d)) * 2.0 ** -8
+    k[30] = -down / d ** 0.5
+    v[30] *= 2.0 ** 22
+    refill(c, k, v)
+    check_rows(c, c.run(), f"down {down}")
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("d,hq,m,kt,vt", [(64, 1, 1, 1, 1), (64, 14, 1, 0, 0), (96, 3, 2, 1, 0), (96, 5, 3, 0, 1),
+                                           (128, 5, 1, 1, 1), (128, 6, 4, 1, 1), (128, 5, 8, 1, 0), (192, 4, 2, 0, 1),
+                                           (256, 4, 1, 1, 1), (256, 3, 8, 0, 0)])
+def test_scales_all_over_the_range(d, hq, m, kt, vt, dtype):
+    """Every block of every token of a size of its own, from 2^-23 to 2^15, zeros among them; then only some tokens."""
+    g = np.random.default_rng(d + hq)
+    for n, some in ((33, 1.0), (500, 1.0), (500, 0.05), (2100, 0.01)):
+        c = Case([n], m, hq, 1, d, kt, vt, dtype=dtype, window=0 if n < 2000 else 900, seed=n)
+        size = 2.0 ** np.where(g.random((n, 1, d // 32, 1)) < some, g.uniform(-20, 15, (n, 1, d // 32, 1)), 0)
+        size *= g.random((n, 1, d // 32, 1)) > 0.1
+        v = (g.standard_normal((n, 1, d // 32, 32)) * size).reshape(n, 1, d)
+        refill(c, g.standard_normal((n, 1, d)), v)
+        check_rows(c, c.run(), f"{n} tokens, {some}")
+
+
+def test_small_values_of_one_size():
+    """Scales of one size anywhere in fp16's range, subnormal ones among them: a power of two brings them up."""
+    g = np.random.default_rng(9)
+    for vt in (0, 1):
+        for size in (2.0 ** -17, 2.0 ** -12, 2.0 ** -6, 1.0, 2.0 ** 6, 2.0 ** 13):
+            c = Case([200], 2, 5, 1, 128, 1, vt, seed=10)
+            refill(c, g.standard_normal((200, 1, 128)), g.standard_normal((200, 1, 128)) * size)
+            check_rows(c, c.run(), f"size {size}")
