@@ -968,7 +968,9 @@ __device__ __forceinline__ void kv_attn_body(const KvLaunch &p, uint32_t *status
         }
         m = make_float2(fmaxf(m.x * factor[o].x, top[o].x), fmaxf(m.y * factor[o].y, top[o].y));
         const float2 ref = make_float2(m.x == -INFINITY ? 0.0f : m.x, m.y == -INFINITY ? 0.0f : m.y);
-        const float2 from13 = make_float2(13.0f - ref.x, 13.0f - ref.y);
+        // Products are rounded as the maximum's was, and 13 less the maximum downwards:
+        // no weight is above 2^13, nor the largest lost, however large the scores.
+        const float2 from13 = make_float2(__fsub_rd(13.0f, ref.x), __fsub_rd(13.0f, ref.y));
         const float2 k = make_float2(exp2_approx(top[o].x - ref.x), exp2_approx(top[o].y - ref.y));
         top[o] = m;
         float2 add = make_float2(0.0f, 0.0f);
@@ -976,7 +978,9 @@ __device__ __forceinline__ void kv_attn_body(const KvLaunch &p, uint32_t *status
         for (int gi = 0; gi < TG; ++gi)
 #pragma unroll
           for (int j = 0; j < 2; ++j) {
-            float2 w = __ffma2_rn(z[o][gi][j], factor[o], from13);
+            // (__fmul_rn one by one: a packed product before a packed sum became one operation)
+            float2 w = make_float2(__fmul_rn(z[o][gi][j].x, factor[o].x), __fmul_rn(z[o][gi][j].y, factor[o].y));
+            w = __fadd2_rn(w, from13);
             w = make_float2(exp2_approx(w.x), exp2_approx(w.y));
             add = __fadd2_rn(add, w);
             z[o][gi][j] = w;

@@ -192,3 +192,34 @@ def test_small_values_of_one_size():
             c = Case([200], 2, 5, 1, 128, 1, vt, seed=10)
             refill(c, g.standard_normal((200, 1, 128)), g.standard_normal((200, 1, 128)) * size)
             check_rows(c, c.run(), f"size {size}")
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("sign", [1.0, -1.0])
+@pytest.mark.parametrize("exp", range(16, 33, 2))
+def test_steep_scores(exp, sign, dtype):
+    """Finite scores up to 2^32: where the largest is far above the others its value is the output."""
+    n, hq, d, seen = 200, 6, 128, 0
+    for seed in range(4):
+        g = np.random.default_rng(100 * exp + seed)
+        c = Case([n], 2, hq, 1, d, 0, 1, dtype=dtype, seed=seed)
+        size = 2.0 ** (exp / 2)
+        refill(c, g.standard_normal((n, 1, d)) * size, g.standard_normal((n, 1, d)))
+        q = torch.from_numpy((g.standard_normal((1, 2, hq, d)) * size).astype(np.float32)).to(dtype)
+        c.q, c.qd = q.double().numpy(), q.cuda()
+        c.scale = sign * d ** -0.5
+        y = c.run().double().cpu().numpy()[0]
+        assert np.isfinite(y).all()
+        k, v = c.kv[0]
+        for i in range(2):
+            for h in range(hq):
+                z = k[:n - 1 + i, 0] @ c.q[0, i, h] * c.scale
+                at = np.argsort(z)[-2:]
+                # scores are off by 16 u sqrt(D) S at most (check_rows); 40 apart leaves 2^-57 for the rest
+                s = (np.abs(k[:n - 1 + i, 0]) @ np.abs(c.q[0, i, h])).max() * abs(c.scale)
+                if z[at[1]] - z[at[0]] > 40 + 32 * U * np.sqrt(d) * s:
+                    want = v[at[1], 0]
+                    seen += 1
+                    assert (np.abs(y[i, h] - want) <= (16 * U * np.sqrt(1 + d) + (2.0 ** -8 + 2.0 ** -10 if dtype == torch.bfloat16 else 0)) * np.abs(want) + 2.0 ** -29).all()
+    assert seen > 10
+    assert qmm.device_status() == 0
