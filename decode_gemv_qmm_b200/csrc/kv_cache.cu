@@ -167,7 +167,7 @@ __device__ __forceinline__ void write_units(const KvForm &f, int64_t tokens, con
       if (!Q8) {
         down = fminf(down, __shfl_xor_sync(0xffffffffu, down, 1));
         down = fminf(down, __shfl_xor_sync(0xffffffffu, down, 2));
-        tie |= up == -down && up != 0.0f;
+        tie |= there && j < k.n && up == -down;  // zeros too: theirs may be of either sign
       }
       top[j] = Q8 || up >= -down ? up : down;
     }
