@@ -200,7 +200,7 @@ __device__ __forceinline__ void write_units(const KvForm &f, int64_t tokens, con
         // The products one by one: a packed product before a packed sum gave other
         // bytes for bf16 rows (as one rounding of both would), and each is rounded here.
         const float2 y = make_float2(__fmul_rn(x[j][e], id), __fmul_rn(x[j][e + 1], id));
-        if (Q8) {  // half away from zero: the number below 0.5 takes halves up and nothing else; |y| < 127.5
+        if (Q8) {  // half away from zero: the number below 0.5 takes halves up and nothing else; |y| < 127.5; where not, see below
           c[e] = static_cast<uint32_t>(__float2int_rz(__fadd_rn(y.x, copysignf(0.49999997f, y.x))));
           c[e + 1] = static_cast<uint32_t>(__float2int_rz(__fadd_rn(y.y, copysignf(0.49999997f, y.y))));
         } else {  // truncated: the sum with 2^23, rounded towards zero, ends in the code
@@ -215,6 +215,23 @@ __device__ __forceinline__ void write_units(const KvForm &f, int64_t tokens, con
         w[(2 * j) & 3] = lo, w[(2 * j + 1) & 3] = hi;
       else
         w[j & 3] = (lo & 0x0f0f0f0fu) | (hi << 4 & 0xf0f0f0f0u);
+    }
+    // Where 1 / d overflows (d below 2^-128) or d is not finite, the rule's clamp acts.
+    if (Q8 && __any_sync(0xffffffffu, isinf(inverse) || !isfinite(scale))) {
+#pragma unroll
+      for (int j = 0; j < kMost; ++j) {
+        const float id = __shfl_sync(0xffffffffu, inverse, (threadIdx.x & 28) + j);
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          uint32_t v = 0;
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const float r = fminf(fmaxf(roundf(__fmul_rn(x[j][4 * h + e], id)), -127.0f), 127.0f);
+            v |= (static_cast<uint32_t>(static_cast<int>(r)) & 255u) << (8 * e);
+          }
+          w[(2 * j + h) & 3] = v;
+        }
+      }
     }
     KvAt at;
     if (!there || !at_slot(f, slot, k.head, val, &at)) continue;
