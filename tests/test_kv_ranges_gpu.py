@@ -223,3 +223,22 @@ def test_steep_scores(exp, sign, dtype):
                     assert (np.abs(y[i, h] - want) <= (16 * U * np.sqrt(1 + d) + (2.0 ** -8 + 2.0 ** -10 if dtype == torch.bfloat16 else 0)) * np.abs(want) + 2.0 ** -29).all()
     assert seen > 10
     assert qmm.device_status() == 0
+
+
+@pytest.mark.parametrize("kt", [0, 1])
+@pytest.mark.parametrize("bits", [0x7c00, 0xfc00, 0x7e00])
+def test_key_scales_that_are_not_finite_stay_with_their_rows(bits, kt):
+    """A key that only the last two of four rows see, and one that the window leaves to the first."""
+    n, m, d = 90, 4, 128
+    for window, at, rows in ((0, n - 2, (0, 1)), (40, n - m - 39, (1, 2, 3))):
+        c = Case([n], m, 3, 1, d, kt, 1, seed=3, window=window)
+        g = np.random.default_rng(4)
+        refill(c, g.standard_normal((n, 1, d)), g.standard_normal((n, 1, d)))
+        plain = ref.Cache(0, 1, d, 16, kt, 1)
+        pg, base, t = plain._base(c.slots[at], 0)
+        c.cache[int(pg), dev(base + plain.at[0][2][t, 1])] = dev(np.array([bits & 255, bits >> 8], np.uint8))
+        y = c.run().double().cpu().numpy()[0]
+        want = ref.attention(c.q[0], *c.kv[0], n, c.scale, window)    # (of the finite key: the rows below do not see it)
+        for i in rows:
+            ref.assert_attention(y[i:i + 1], tuple(x[i:i + 1] if isinstance(x, np.ndarray) and x.ndim else x for x in want), f"row {i}")
+    assert qmm.device_status() == 0
