@@ -89,7 +89,7 @@ __host__ __device__ constexpr int64_t kv_attn_slot_floats(int rows, int d) { ret
 constexpr int kKvMaxBlocks = 160;  // most blocks of a launch
 constexpr int kKvMaxWarps = 8;     // most warps of a block
 // What beginning an item costs a warp, in groups of keys (16 sequences of 6 to 100
-// tokens: 16 us with 4, 26 us with 2; 64 long ones: 103 and 106 us).
+// tokens: 15.6 us with 4, 21.6 us with 2; 64 long ones: 101.8 and 103.3 us).
 constexpr int kKvItemCost = 4;
 
 // Scratch: two marks and two partial results of each block, two outputs of each warp.
@@ -109,12 +109,13 @@ struct KvCfg {
   static constexpr int kBudget = 216 * 1024;  // of 227 KB; the rest is the static arrays
   static constexpr int warp_bytes(int tg, int stages) { return kQBytes + stages * tg * kGroupBytes; }
   // Warps of a block, one block an SM. 12 and 16 warps of fewer registers and
-  // shorter steps were as fast or slower: instructions bound the kernel, not their
-  // latency.
+  // shorter steps were as fast or slower.
   static constexpr int kNW = 8 * warp_bytes(1, 2) <= kBudget ? 8 : 4;
-  // Groups of a step, as many as leave the sums in registers: 64 ragged sequences
-  // of up to 8192 tokens took 99, 105, 126 us with 4, 2, 1 (one octet of rows). A
-  // step's ring stage is 9 KB at most, so that two to four are in flight.
+  // Groups of a step, as many as leave the sums in registers (ptxas reports 255 of
+  // them and 12 to 28 bytes spilled for one octet of fp32 rows of 128, Q4_0): 64
+  // ragged sequences of up to 8192 tokens take 102, 117, 144 us with 4, 2, 1 (one
+  // octet of rows), 131072 keys of one 55, 63, 76 us. A step's ring stage is 9 KB at
+  // most, so that two to four are in flight.
   static constexpr int kMaxTG = OCT == 1 ? 4 : OCT == 2 ? 2 : 1;
   static constexpr bool fits(int tg) { return tg * kGroupBytes <= 9216 && kNW * warp_bytes(tg, 2) <= kBudget; }
   static constexpr int kTG = kMaxTG >= 4 && fits(4) ? 4 : kMaxTG >= 2 && fits(2) ? 2 : 1;
@@ -412,9 +413,12 @@ __device__ __noinline__ void kv_add_apart_call(KvApart<NB, OCT, TG> &s, uint32_t
 // columns: scores are keys x rows, outputs dims x rows, so a conversion serves
 // every octet and no column is wasted on terms. fp32 queries (FINE) and the
 // weights that go with them are two fp16 terms (22 bits together), each a product
-// of its own into the same sums; bf16 queries and their weights are one. A key's
-// block scale multiplies the finished 32-dim dot in fp32; a value's block scale
-// goes into the weight, p d_v, in fp16 with the product's own remainder (FINE).
+// of its own into the same sums; bf16 queries and their weights are one (the
+// weights' remainders would take 2 to 6% of short calls and 8 to 25% of long ones,
+// and bring the outputs' error, 1.674e-3 of their norm, to bf16's own 1.672e-3). A
+// key's block scale multiplies the finished 32-dim dot in fp32; a value's block scale
+// goes into the weight, p d_v, in fp16 with the product's own remainder (FINE), or, in
+// steps whose scales lie far apart or are not finite, in fp32 (kv_add_apart).
 // The weights change sides between the two products by 8 x 8 transposes. Each
 // step's sums are added to fp32 registers outside the tensor core, whose own sums
 // need not be rounded to nearest.
@@ -423,11 +427,13 @@ __device__ __noinline__ void kv_add_apart_call(KvApart<NB, OCT, TG> &s, uint32_t
 // of two heads: 2 us to know the lengths and find the work, 1 us for the first
 // copies, 1 to 2 us a step and again for joining); at long ones instructions. 16
 // keys of a head of 128, Q4_0, fp32 queries, are 370 instructions of a warp: 132
-// on the 2-cycle ALU, 111 in fp16 (2 cycles), 32 products of 8 cycles in which,
-// measured, nothing else is issued, some 740 cycles together. One
-// sequence of 131072 tokens, 8 heads: 54 us, 2.8 TB/s of cache (29 us without the
-// arithmetic); 16 x 8192 tokens, 8 heads of 256, Q8_0, where a byte needs half the
-// instructions: 109 us, 5.2 TB/s, 80% of the measured copy rate.
+// on the 2-cycle ALU, 111 in fp16 (2 cycles), 32 products of 8 cycles, which overlap
+// by a third; some 710 cycles together. One
+// sequence of 131072 tokens, 8 heads: 54.6 us, 2.8 TB/s of cache (29 us without the
+// arithmetic), of which some 13 us are the call's own: with one step a warp (8192
+// tokens) it takes 16.2 us, and a step more takes 3 us. 16 x 8192 tokens, 8 heads of 256, Q8_0, one query row,
+// where a byte needs half the instructions: 110 us, 5.2 TB/s, 79% of the measured
+// copy rate.
 template <int NB, bool KQ8, bool VQ8, int OCT, bool FINE>
 __device__ __forceinline__ void kv_attn_body(const KvLaunch &p, uint32_t *status) {
   using C = KvCfg<NB, KQ8, VQ8, OCT, FINE>;
@@ -1238,11 +1244,11 @@ cudaError_t kv_attn_launch(const DevInfo &dev, KvLaunch &p, uint32_t *status, cu
   return cudaLaunchKernelEx(&cfg, kernel, p, status);
 }
 
-// Octets of rows that a warp takes at a time: all of them while their sums stay
-// in registers, else two. 16 x 8192 keys of 8 heads of 128, Q4_0, took for 1, 2,
-// 3, 4 octets at a time 55, 87, 136, 188 us with fp32 queries (so four are better
-// as two and two) and 47, 67, 101, 130 us with bf16; five to eight as twos are
-// within 3% of the best split.
+// Octets of rows that a warp takes at a time: all of them while most of their sums
+// stay in registers (three of 128 with fp32 queries spill 76 bytes, four with bf16
+// ones 112, two of 256 up to 236), else two. 16 x 8192 keys of 8 heads of 128, Q4_0,
+// take for 1, 2, 3, 4 octets at a time 55, 88, 141, 195 us with fp32 queries (four as
+// two and two 160) and 47, 68, 107, 143 us with bf16.
 constexpr int kv_attn_octets(int nb, int rows, bool fine) {
   const int need = (rows + 7) / 8, most = nb > 4 ? 2 : fine ? 3 : 4;
   return need <= most ? need : 2;
@@ -1262,7 +1268,8 @@ cudaError_t kv_attn_rows(const DevInfo &dev, KvLaunch &p, uint32_t *status, cons
   }
 }
 
-// fp32 queries in two fp16 terms, bf16 ones (whose outputs keep 8 bits) in one.
+// fp32 queries in two fp16 terms, bf16 ones (whose outputs keep 8 bits) in one, and
+// the weights with them.
 template <int NB, bool KQ8, bool VQ8>
 cudaError_t kv_attn_dtype(const DevInfo &dev, KvLaunch &p, uint32_t *status, const cudaLaunchConfig_t &cfg) {
   return p.bf16 ? kv_attn_rows<NB, KQ8, VQ8, false>(dev, p, status, cfg)

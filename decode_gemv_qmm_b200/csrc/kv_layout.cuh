@@ -39,7 +39,7 @@ __host__ __device__ constexpr int kv_part_bytes(int nb, bool q8) { return kv_cod
 // The runs of blocks of a row: how many, a run's first block and its blocks. Plain
 // arithmetic on the run's number, which unrolled loops fold: a loop that steps by
 // a run's length is not unrolled, and arrays indexed in it lie in local memory
-// (attention over 16 x 8192 tokens of 8 heads of 256, Q8_0: 268 us, with this 109).
+// (attention over 16 x 8192 tokens of 8 heads of 256, Q8_0: 268 us, with this 110).
 __host__ __device__ constexpr int kv_runs(int nb, bool q8) { return q8 ? nb / 2 + nb % 2 : nb / 4 + nb % 4 / 2 + nb % 2; }
 __host__ __device__ constexpr int kv_run_first(int nb, bool q8, int i) {
   return q8 ? 2 * i : nb % 4 == 3 && i == nb / 4 + 1 ? nb - 1 : 4 * i;

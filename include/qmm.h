@@ -375,8 +375,11 @@ QMM_API qmm_status qmm_quant_matmul_prefill_ex(int wtype, int64_t M, int64_t N, 
  * Keys and values of a decoder's tokens, held in the block formats of the
  * weights (Q8_0 or Q4_0, keys and values each of their own type), written as
  * tokens arrive and read where they lie by the attention. Element types: fp32
- * (the decode path's) or bf16 (the prefill path's); sums, maxima and products
- * are fp32 either way.
+ * (the decode path's) or bf16 (the prefill path's). Scores, maxima and sums are
+ * fp32 either way. fp32 queries, and the weights of the values with them, are held
+ * in 22 bits or more; with bf16 queries the weights are rounded to fp16 twice (the
+ * weight, and its product with a value's block scale: 2^-11 each, together a
+ * quarter of the bf16 output's own rounding).
  *
  * Form of a cache, common to the calls below:
  *   ktype, vtype  QMM_Q8_0 or QMM_Q4_0 (QMM_ERR_DTYPE otherwise)
@@ -419,8 +422,10 @@ QMM_API qmm_status qmm_kv_page_bytes(int ktype, int vtype, int64_t Hkv, int64_t 
  * Each 32-block of a row by ggml's rules, every step an IEEE binary32
  * operation: Q8_0 as qmm_quantize_act_q8_0; Q4_0 with m the first x_j of
  * largest magnitude, d = m / -8, id = 1 / d (0 when d == 0), q_j = min(15,
- * trunc(x_j * id + 8.5)). The scale is stored as binary16(d), rounded to
- * nearest even. The stored bytes are a function of the row alone.
+ * trunc(x_j * id + 8.5)), held in 0 .. 15 where id is infinite. The scale is
+ * stored as binary16(d), rounded to nearest even (above 65504: infinity). The
+ * stored bytes are a function of the row alone; those of a block that holds a NaN
+ * are unspecified.
  *
  *   dtype     QMM_F32 or QMM_BF16: elements of K and V
  *   T         tokens, >= 0
@@ -464,7 +469,10 @@ QMM_API qmm_status qmm_kv_read(int ktype, int vtype, int dtype, int64_t T, int64
  * neither is, for a row, any other token that it does not see: a value that is
  * not finite (an input above 524000 in magnitude has no finite Q4_0 scale)
  * makes the outputs of its block infinite or NaN in the rows that see it, and
- * in no other.
+ * in no other. How far an output is off goes by the values that its row
+ * sees in its own dim, whatever the sizes of others. The same call gives the
+ * same bits every time; a sequence beside others may get others in the last
+ * places, since the work is split over the whole call.
  *
  *   dtype     QMM_F32 or QMM_BF16: elements of Q and Y
  *   B, M      sequences (<= QMM_KV_MAX_BATCH) and query tokens of each
@@ -482,7 +490,7 @@ QMM_API qmm_status qmm_kv_read(int ktype, int vtype, int dtype, int64_t T, int64
  *   Y         B x M x Hq x D (device, 16-byte aligned, written)
  *   ws        ws_bytes >= qmm_kv_attn_workspace(...) bytes of scratch (device,
  *             16-byte aligned, no contents needed before or after); one call at
- *             a time may use it
+ *             a time may use it. Y and ws overlap no other argument
  * A position whose page does not exist is left out, a length outside the range
  * is taken as the nearest one in it; both are recorded (qmm_device_status).
  */
@@ -493,7 +501,9 @@ QMM_API qmm_status qmm_kv_attn(int ktype, int vtype, int dtype, int64_t B, int64
                                int64_t window, void *Y, void *ws, int64_t ws_bytes, qmm_stream_t stream);
 
 /* qmm_kv_attn_workspace -- scratch bytes that qmm_kv_attn needs for these sizes
- * (host only, needs no device). *bytes: host, written. */
+ * (host only, needs no device). *bytes: host, written. The same for every B: two
+ * partial results of each block and of each warp of the launch (12.5 MB for up to
+ * 8 query rows, M * Hq / Hkv, of 128, 50 MB at most). */
 QMM_API qmm_status qmm_kv_attn_workspace(int64_t B, int64_t M, int64_t Hq, int64_t Hkv, int64_t D, int64_t *bytes);
 
 /* ------------------------------------------------------------------------ */
