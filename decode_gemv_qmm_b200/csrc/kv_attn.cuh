@@ -428,12 +428,11 @@ __device__ __noinline__ void kv_add_apart_call(KvApart<NB, OCT, TG> &s, uint32_t
 // copies, 1 to 2 us a step and again for joining); at long ones instructions. 16
 // keys of a head of 128, Q4_0, fp32 queries, are 370 instructions of a warp: 132
 // on the 2-cycle ALU, 111 in fp16 (2 cycles), 32 products of 8 cycles, which overlap
-// by a third; some 710 cycles together. One
-// sequence of 131072 tokens, 8 heads: 54.6 us, 2.8 TB/s of cache (29 us without the
-// arithmetic), of which some 13 us are the call's own: with one step a warp (8192
-// tokens) it takes 16.2 us, and a step more takes 3 us. 16 x 8192 tokens, 8 heads of 256, Q8_0, one query row,
-// where a byte needs half the instructions: 110 us, 5.2 TB/s, 79% of the measured
-// copy rate.
+// by a third; some 710 cycles together. One sequence of 131072 tokens, 8 heads: 54.6
+// us, 2.8 TB/s of cache (29 us without the arithmetic), of which some 13 us are the
+// call's own: with one step a warp (8192 tokens) it takes 16.2 us, and a step more
+// takes 3 us. 16 x 8192 tokens, 8 heads of 256, Q8_0, one query row, where a byte needs
+// half the instructions: 110 us, 5.2 TB/s, 79% of the measured copy rate.
 template <int NB, bool KQ8, bool VQ8, int OCT, bool FINE>
 __device__ __forceinline__ void kv_attn_body(const KvLaunch &p, uint32_t *status) {
   using C = KvCfg<NB, KQ8, VQ8, OCT, FINE>;

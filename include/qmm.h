@@ -377,9 +377,10 @@ QMM_API qmm_status qmm_quant_matmul_prefill_ex(int wtype, int64_t M, int64_t N, 
  * tokens arrive and read where they lie by the attention. Element types: fp32
  * (the decode path's) or bf16 (the prefill path's). Scores, maxima and sums are
  * fp32 either way. fp32 queries, and the weights of the values with them, are held
- * in 22 bits or more; with bf16 queries the weights are rounded to fp16 twice (the
- * weight, and its product with a value's block scale: 2^-11 each, together a
- * quarter of the bf16 output's own rounding).
+ * in 22 bits or more (a weight that is small beside its row's largest: to 2^-29 of
+ * that one); with bf16 queries the weights are rounded to fp16 twice (the weight,
+ * and its product with a value's block scale: 2^-11 each, together a quarter of the
+ * bf16 output's own rounding).
  *
  * Form of a cache, common to the calls below:
  *   ktype, vtype  QMM_Q8_0 or QMM_Q4_0 (QMM_ERR_DTYPE otherwise)

@@ -31,10 +31,11 @@ def take(c, hkv, d):
 def check_rows(c, y, what=""):
     """Per output, with A = sum p|v| / sum p over the keys the row sees and S the row's largest sum |scale q_d k_jd|:
     (16 u sqrt(D) S + 16 u sqrt(1 + D)) A as kv_reference.assert_attention derives it, and the floor of fp16 terms. There
-    a weight p d_v is off by less than 2^-36 for scales d_v in [2^-7, 2) (and where scales are brought there by a power
-    of two, that much of it); a code c makes that 2^-36 |c| <= 2^-29 |c| d_v = 2^-29 |v|, of every key the row sees. bf16:
-    2^-10 A (weights) and 2^-8 of the output besides. Where a seen value is not finite, what 64 bits give: the same
-    infinity, or NaN."""
+    a weight's terms lose at most half of fp16's smallest step, 2^-25, where p 2^13 is split and twice where its product
+    with d_v is, 2^-38 (d_v + 2) of p d_v's unit; for scales d_v of 2^-7 and more (or brought there by a power of two,
+    which goes into both) and a code c that is 2^-38 (1 + 2 / d_v) |c| d_v <= 2^-38 257 |v| < 2^-29 |v|, of every key the
+    row sees. bf16: 2^-10 A (weights) and 2^-8 of the output besides. Where a seen value is not finite, what 64 bits give:
+    the same infinity, or NaN."""
     y = y.double().cpu().numpy()[0]
     q, (k, v), n = c.q[0], c.kv[0], c.lens[0]
     m, hq, d = q.shape
